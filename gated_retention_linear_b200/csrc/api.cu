@@ -10,6 +10,7 @@
 #include "gn_gate.cuh"
 #include "prefill_ew.cuh"
 #include "swa.cuh"
+#include "paged.cuh"
 
 using namespace gret;
 
@@ -404,3 +405,244 @@ extern "C" gret_status_t gret_swa_decode_step(const void* q, const void* k, cons
     if (e == cudaErrorInvalidValue) return GRET_ERR_UNSUPPORTED;
     return e == cudaSuccess ? GRET_OK : GRET_ERR_CUDA;
 }
+
+// ---- paged key-value cache
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks shared by the paged entry points.  Sizes first, then pointers, then alignment.
+gret_status_t paged_table(const int32_t* page_table, int64_t stride, int max_pages, int S,
+                          PagedTable& t) {
+    if (S < 0 || max_pages < 1 || stride < max_pages) return GRET_ERR_INVALID_ARG;
+    if (S > PAGED_MAX_SEQS) return GRET_ERR_UNSUPPORTED;
+    if (S > 0 && !page_table) return GRET_ERR_INVALID_ARG;
+    if (!aligned4(page_table)) return GRET_ERR_ALIGNMENT;
+    t.entries = const_cast<int32_t*>(page_table);
+    t.stride = stride;
+    t.max_pages = max_pages;
+    t.S = S;
+    return GRET_OK;
+}
+
+gret_status_t paged_sizes(int n_pages, int page_size, int max_pages, int& shift) {
+    if (n_pages < 1 || page_size < 1) return GRET_ERR_INVALID_ARG;
+    if (n_pages > 1 << 30 || page_size > PAGED_MAX_PAGE || (page_size & (page_size - 1)))
+        return GRET_ERR_UNSUPPORTED;
+    // lengths are int32
+    if (max_pages > 0 && (int64_t)max_pages * page_size > 0x7fffffffLL) return GRET_ERR_UNSUPPORTED;
+    shift = 0;
+    while (1 << shift < page_size) ++shift;
+    return GRET_OK;
+}
+
+gret_status_t paged_pool(const void* k_pages, const void* v_pages, int64_t sp, int64_t st,
+                         int64_t sh, gret_dtype_t dtype, int n_pages, int page_size, int max_pages,
+                         int Hkv, int d, PagedPool& p) {
+    if (dtype != GRET_F32 && dtype != GRET_BF16) return GRET_ERR_INVALID_ARG;
+    if (Hkv < 1 || d < 1 || sp < 0 || st < 0 || sh < 0) return GRET_ERR_INVALID_ARG;
+    const gret_status_t s = paged_sizes(n_pages, page_size, max_pages, p.page_shift);
+    if (s != GRET_OK) return s;
+    if (!k_pages || !v_pages) return GRET_ERR_INVALID_ARG;
+    const int64_t es = dtype == GRET_BF16 ? 2 : 4;
+    if (sp > INT64_MAX / es / n_pages || st > INT64_MAX / es / page_size || sh > INT64_MAX / es / Hkv)
+        return GRET_ERR_INVALID_ARG;
+    if (d > 65536 || (int64_t)Hkv * d * page_size > 0x0fffffffLL) return GRET_ERR_UNSUPPORTED;
+    if (d * es % 16 || sp * es % 16 || st * es % 16 || sh * es % 16 || !aligned16(k_pages) ||
+        !aligned16(v_pages))
+        return GRET_ERR_ALIGNMENT;
+    p.k = static_cast<unsigned char*>(const_cast<void*>(k_pages));
+    p.v = static_cast<unsigned char*>(const_cast<void*>(v_pages));
+    p.sp = sp * es;
+    p.st = st * es;
+    p.sh = sh * es;
+    p.n_pages = n_pages;
+    p.H = Hkv;
+    p.row_bytes = (int)(d * es);
+    return GRET_OK;
+}
+
+gret_status_t launched(cudaError_t e) { return e == cudaSuccess ? GRET_OK : GRET_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+size_t gret_paged_attention_workspace_size(gret_dtype_t dtype, int Hq, int Hkv, int d) {
+    if ((dtype != GRET_F32 && dtype != GRET_BF16) || Hkv < 1 || Hq < 1 || Hq % Hkv || !dim_ok(d))
+        return 0;
+    return paged_attn_workspace(dtype == GRET_BF16, Hq, Hkv, d);
+}
+
+gret_status_t gret_paged_attention_decode(
+    const void* q, const int32_t* seq_lens, const int32_t* page_table, int64_t table_stride,
+    int max_pages, const void* k_pages, const void* v_pages, int64_t stride_page,
+    int64_t stride_tok, int64_t stride_head, int n_pages, int page_size, gret_dtype_t dtype,
+    float scale, int window, int B, int Hq, int Hkv, int d, void* o, float* lse, int32_t* status,
+    void* workspace, size_t workspace_bytes, gret_stream_t stream) {
+    const NvtxRange range("gret_paged_attention_decode");
+    PagedAttnArgs a;
+    if (!isfinite(scale) || window < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv)
+        return GRET_ERR_INVALID_ARG;
+    gret_status_t s = paged_table(page_table, table_stride, max_pages, B, a.table);
+    if (s != GRET_OK) return s;
+    s = paged_pool(k_pages, v_pages, stride_page, stride_tok, stride_head, dtype, n_pages,
+                   page_size, max_pages, Hkv, d, a.pool);
+    if (s != GRET_OK) return s;
+    if (!dim_ok(d) || (int64_t)B * Hq > 0x7fffffffLL) return GRET_ERR_UNSUPPORTED;
+    if (B == 0) return GRET_OK;
+    if (!q || !seq_lens || !o) return GRET_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(seq_lens) || !aligned4(lse) ||
+        !aligned4(status) || !aligned16(workspace))
+        return GRET_ERR_ALIGNMENT;
+    if (!workspace ||
+        workspace_bytes < paged_attn_workspace(dtype == GRET_BF16, Hq, Hkv, d))
+        return GRET_ERR_WORKSPACE;
+    a.q = q;
+    a.seq_lens = seq_lens;
+    a.bf16 = dtype == GRET_BF16;
+    a.scale = scale;
+    a.window = window;
+    a.Hq = Hq;
+    a.d = d;
+    a.o = o;
+    a.lse = lse;
+    a.status = status;
+    a.workspace = workspace;
+    return launched(launch_paged_attn(a, (cudaStream_t)stream));
+}
+
+gret_status_t gret_paged_append(
+    const void* k, int64_t k_stride_tok, int64_t k_stride_head, const void* v,
+    int64_t v_stride_tok, int64_t v_stride_head, int64_t T, const int32_t* cu_seqlens,
+    const int32_t* pos, int S, const int32_t* page_table, int64_t table_stride, int max_pages,
+    void* k_pages, void* v_pages, int64_t stride_page, int64_t stride_tok, int64_t stride_head,
+    int n_pages, int page_size, gret_dtype_t dtype, int Hkv, int d, int32_t* status,
+    gret_stream_t stream) {
+    const NvtxRange range("gret_paged_append");
+    PagedAppendArgs a;
+    if (T < 0 || k_stride_tok < 0 || k_stride_head < 0 || v_stride_tok < 0 || v_stride_head < 0)
+        return GRET_ERR_INVALID_ARG;
+    if (!cu_seqlens && T != S) return GRET_ERR_INVALID_ARG;
+    gret_status_t s = paged_table(page_table, table_stride, max_pages, S, a.table);
+    if (s != GRET_OK) return s;
+    s = paged_pool(k_pages, v_pages, stride_page, stride_tok, stride_head, dtype, n_pages,
+                   page_size, max_pages, Hkv, d, a.pool);
+    if (s != GRET_OK) return s;
+    if (T > 0x7fffffffLL) return GRET_ERR_UNSUPPORTED;   // positions in cu_seqlens are int32
+    if (T == 0 || S == 0) return GRET_OK;
+    if (!k || !v || !pos) return GRET_ERR_INVALID_ARG;
+    const int64_t es = dtype == GRET_BF16 ? 2 : 4;
+    if (k_stride_tok > INT64_MAX / es / T || v_stride_tok > INT64_MAX / es / T ||
+        k_stride_head > INT64_MAX / es / Hkv || v_stride_head > INT64_MAX / es / Hkv)
+        return GRET_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || k_stride_tok * es % 16 || k_stride_head * es % 16 ||
+        v_stride_tok * es % 16 || v_stride_head * es % 16 || !aligned4(cu_seqlens) ||
+        !aligned4(pos) || !aligned4(status))
+        return GRET_ERR_ALIGNMENT;
+    a.k = static_cast<const unsigned char*>(k);
+    a.v = static_cast<const unsigned char*>(v);
+    a.kt = k_stride_tok * es;
+    a.kh = k_stride_head * es;
+    a.vt = v_stride_tok * es;
+    a.vh = v_stride_head * es;
+    a.T = T;
+    a.cu_seqlens = cu_seqlens;
+    a.pos = pos;
+    a.status = status;
+    return launched(launch_paged_append(a, (cudaStream_t)stream));
+}
+
+size_t gret_paged_resize_workspace_size(int S) {
+    return S < 0 || S > PAGED_MAX_SEQS ? 0 : ((size_t)S * 4 + 15) / 16 * 16;
+}
+
+gret_status_t gret_paged_resize(
+    const int32_t* delta, int32_t* seq_lens, int S, int32_t* page_table, int64_t table_stride,
+    int max_pages, int32_t* ref, void* k_pages, void* v_pages, int64_t stride_page,
+    int64_t stride_tok, int64_t stride_head, int n_pages, int page_size, gret_dtype_t dtype,
+    int Hkv, int d, int32_t* pos, int32_t* status, void* workspace, size_t workspace_bytes,
+    gret_stream_t stream) {
+    const NvtxRange range("gret_paged_resize");
+    PagedResizeArgs a;
+    gret_status_t s = paged_table(page_table, table_stride, max_pages, S, a.table);
+    if (s != GRET_OK) return s;
+    s = paged_pool(k_pages, v_pages, stride_page, stride_tok, stride_head, dtype, n_pages,
+                   page_size, max_pages, Hkv, d, a.pool);
+    if (s != GRET_OK) return s;
+    if (S == 0) return GRET_OK;
+    if (!delta || !seq_lens || !ref || !pos) return GRET_ERR_INVALID_ARG;
+    if (!aligned4(delta) || !aligned4(seq_lens) || !aligned4(ref) || !aligned4(pos) ||
+        !aligned4(status) || !aligned16(workspace))
+        return GRET_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < gret_paged_resize_workspace_size(S))
+        return GRET_ERR_WORKSPACE;
+    a.delta = delta;
+    a.seq_lens = seq_lens;
+    a.pos = pos;
+    a.ref = ref;
+    a.status = status;
+    a.workspace = static_cast<int32_t*>(workspace);
+    return launched(launch_paged_resize(a, (cudaStream_t)stream));
+}
+
+gret_status_t gret_paged_fork(
+    const int32_t* src, const int32_t* dst, int n, int32_t* seq_lens, int S, int32_t* page_table,
+    int64_t table_stride, int max_pages, int32_t* ref, int n_pages, int page_size, int32_t* status,
+    gret_stream_t stream) {
+    const NvtxRange range("gret_paged_fork");
+    PagedForkArgs a;
+    if (n < 0) return GRET_ERR_INVALID_ARG;
+    gret_status_t s = paged_table(page_table, table_stride, max_pages, S, a.table);
+    if (s != GRET_OK) return s;
+    s = paged_sizes(n_pages, page_size, max_pages, a.page_shift);
+    if (s != GRET_OK) return s;
+    if (n > PAGED_MAX_SEQS) return GRET_ERR_UNSUPPORTED;
+    if (n == 0 || S == 0) return GRET_OK;
+    if (!src || !dst || !seq_lens || !ref) return GRET_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(dst) || !aligned4(seq_lens) || !aligned4(ref) ||
+        !aligned4(status))
+        return GRET_ERR_ALIGNMENT;
+    a.src = src;
+    a.dst = dst;
+    a.n = n;
+    a.seq_lens = seq_lens;
+    a.ref = ref;
+    a.n_pages = n_pages;
+    a.status = status;
+    return launched(launch_paged_fork(a, (cudaStream_t)stream));
+}
+
+size_t gret_paged_compact_workspace_size(int n_pages) {
+    return n_pages < 1 || n_pages > 1 << 30 ? 0 : (((size_t)n_pages * 3 + 4) * 4 + 15) / 16 * 16;
+}
+
+gret_status_t gret_paged_compact(
+    const int32_t* seq_lens, int S, int32_t* page_table, int64_t table_stride, int max_pages,
+    int32_t* ref, void* k_pages, void* v_pages, int64_t stride_page, int64_t stride_tok,
+    int64_t stride_head, int n_pages, int page_size, gret_dtype_t dtype, int Hkv, int d,
+    int32_t* n_live, int32_t* status, void* workspace, size_t workspace_bytes,
+    gret_stream_t stream) {
+    const NvtxRange range("gret_paged_compact");
+    PagedCompactArgs a;
+    gret_status_t s = paged_table(page_table, table_stride, max_pages, S, a.table);
+    if (s != GRET_OK) return s;
+    s = paged_pool(k_pages, v_pages, stride_page, stride_tok, stride_head, dtype, n_pages,
+                   page_size, max_pages, Hkv, d, a.pool);
+    if (s != GRET_OK) return s;
+    if (!ref || !n_live || (S > 0 && !seq_lens)) return GRET_ERR_INVALID_ARG;
+    if (!aligned4(seq_lens) || !aligned4(ref) || !aligned4(n_live) || !aligned4(status) ||
+        !aligned16(workspace))
+        return GRET_ERR_ALIGNMENT;
+    if (!workspace || workspace_bytes < gret_paged_compact_workspace_size(n_pages))
+        return GRET_ERR_WORKSPACE;
+    a.seq_lens = seq_lens;
+    a.ref = ref;
+    a.n_live = n_live;
+    a.status = status;
+    a.workspace = static_cast<int32_t*>(workspace);
+    return launched(launch_paged_compact(a, (cudaStream_t)stream));
+}
+
+}  // extern "C"

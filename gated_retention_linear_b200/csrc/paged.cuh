@@ -1,0 +1,120 @@
+// paged.cuh -- host interface of the paged key-value cache: decode attention over it
+// (paged_attention.cu) and its upkeep (paged_cache.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gret.h"
+
+namespace gret {
+
+constexpr int PAGED_MAX_PAGE = 1024;      // tokens a page; a power of two
+constexpr int PAGED_MAX_SEQS = 16384;     // rows of a page table: the plan kernels keep 8 bytes of
+                                          // each row in shared memory
+
+// The pool: row (token slot t, head h) of page p is row_bytes bytes at k + p*sp + t*st + h*sh.
+// All strides are in bytes here.
+struct PagedPool {
+    unsigned char* k;
+    unsigned char* v;
+    int64_t sp, st, sh;
+    int n_pages;
+    int page_shift;      // log2(page size)
+    int H;               // heads of a slot
+    int row_bytes;       // a multiple of 16
+};
+
+// The page table: entry j of row s at entries[s * stride + j], j < max_pages.
+struct PagedTable {
+    int32_t* entries;
+    int64_t stride;
+    int max_pages;
+    int S;
+};
+
+struct PagedAttnArgs {
+    const void* q;           // [B, Hq, d]
+    const int32_t* seq_lens; // [B]
+    PagedTable table;        // S = B
+    PagedPool pool;          // H = Hkv
+    bool bf16;
+    float scale;
+    int window;              // 0: no window
+    int Hq, d;
+    void* o;                 // [B, Hq, d]
+    float* lse;              // [B, Hq] or nullptr
+    int32_t* status;         // or nullptr
+    void* workspace;
+};
+
+size_t paged_attn_workspace(bool bf16, int Hq, int Hkv, int d);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+
+struct PagedAppendArgs {
+    const unsigned char* k;  // token i, head h at k + i*kt + h*kh (bytes)
+    const unsigned char* v;
+    int64_t kt, kh, vt, vh;
+    int64_t T;
+    const int32_t* cu_seqlens;  // [S + 1] or nullptr (token i belongs to row i)
+    const int32_t* pos;         // [S]
+    PagedTable table;
+    PagedPool pool;
+    int32_t* status;
+};
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream);
+
+struct PagedResizeArgs {
+    const int32_t* delta;    // [S]
+    int32_t* seq_lens;       // [S]
+    int32_t* pos;            // [S]
+    int32_t* ref;            // [n_pages]
+    PagedTable table;
+    PagedPool pool;
+    int32_t* status;
+    int32_t* workspace;      // [S]
+};
+
+cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream);
+
+struct PagedForkArgs {
+    const int32_t* src;      // [n]
+    const int32_t* dst;      // [n]
+    int n;
+    int32_t* seq_lens;       // [S]
+    int32_t* ref;            // [n_pages]
+    PagedTable table;
+    int n_pages, page_shift;
+    int32_t* status;
+};
+
+cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream);
+
+struct PagedCompactArgs {
+    const int32_t* seq_lens; // [S]
+    int32_t* ref;            // [n_pages]
+    int32_t* n_live;         // [1]
+    PagedTable table;
+    PagedPool pool;
+    int32_t* status;
+    int32_t* workspace;      // 4 + 3 * n_pages
+};
+
+cudaError_t launch_paged_compact(const PagedCompactArgs& a, cudaStream_t stream);
+
+}  // namespace gret
+
+#ifdef __CUDACC__
+namespace gret {
+
+__device__ __forceinline__ void paged_flag(int32_t* status, int bit) {
+    if (status) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ int pages_of(int64_t n, int page_shift) {
+    return (int)((n + (1 << page_shift) - 1) >> page_shift);
+}
+
+}  // namespace gret
+#endif

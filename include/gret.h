@@ -325,6 +325,122 @@ gret_status_t gret_swa_decode_step(const void* q, const void* k, const void* v, 
                                    int window, int B, int H, int d, const int32_t* pos,
                                    void* k_cache, void* v_cache, void* o, gret_stream_t stream);
 
+/*
+ * ---- Paged key-value cache -----------------------------------------------------------------
+ *
+ * The Cross-Decoder's side of serving: one global cache of keys and values that every cross layer
+ * reads (same page, section "Cross-Decoder": 24 query and 8 key-value heads), kept in pages so
+ * that requests of any length share one pool.
+ *
+ *   k_pages, v_pages  the pool: n_pages pages of page_size token slots of Hkv heads of d values.
+ *                     Slot t, head h of page p starts at element p * stride_page + t * stride_tok
+ *                     + h * stride_head of each (both orders of tokens and heads are strides).
+ *   page_table        int32 [S, max_pages], row s at page_table + s * table_stride.  Token t of
+ *                     sequence s lies in slot t % page_size of page page_table[s][t / page_size].
+ *   seq_lens          int32 [S], tokens of each sequence.  Entries of a row past
+ *                     ceil(seq_lens[s] / page_size) are never read.
+ *   ref               int32 [n_pages], the number of sequences that hold a page.  0 means free:
+ *                     nothing else says so, and a pool starts with zeros.
+ *   status            one int32 on the device, or NULL.  Kernels OR GRET_PAGED_* bits into it and
+ *                     never clear it; what a bit reports was left out, nothing out of range is
+ *                     read or written.
+ *
+ * page_size is a power of two up to 1024, S <= 16384, n_pages <= 2^30 (GRET_ERR_UNSUPPORTED
+ * otherwise).  k_pages, v_pages, the strides in bytes and d values in bytes are multiples of 16;
+ * the int32 arrays are 4-byte aligned, workspaces 16-byte aligned (GRET_ERR_ALIGNMENT).  Every
+ * entry point is a fixed sequence of launches whatever the device data, so it can be captured into
+ * a graph and replayed on new lengths; calls that share a workspace must not overlap.
+ * Results do not depend on timing.
+ */
+enum {
+    GRET_PAGED_BAD_PAGE = 1,    /* a page id outside [0, n_pages): its tokens were left out     */
+    GRET_PAGED_BAD_LENGTH = 2,  /* a length or position that the table cannot hold              */
+    GRET_PAGED_NO_PAGES = 4,    /* the pool ran out: the row was not grown                      */
+    GRET_PAGED_TABLE_FULL = 8,  /* a row would pass max_pages: it was not grown                 */
+    GRET_PAGED_BAD_ROW = 16,    /* a pair of gret_paged_fork was refused                        */
+    GRET_PAGED_BAD_COUNT = 32   /* a page that is held has ref 0                                */
+};
+
+/*
+ * Attention of one new token per sequence over the paged cache.  Query head i reads kv head
+ * i / (Hq / Hkv).  With n = seq_lens[b] (the new token's key and value already in the cache):
+ *   o[b, i] = sum_j softmax_j(scale q[b, i] . k_j) v_j  over j in [max(0, n - window), n)
+ *   lse[b, i] = ln sum_j e^(scale q . k_j)              (lse may be NULL)
+ * window = 0 means no window; pages wholly before the window are not read, so they may be gone.
+ * A sequence of length 0 gives o = 0, lse = -inf.  A length past max_pages * page_size is cut off
+ * there (BAD_LENGTH).  Keys on a bad page are left out; a sequence that has no others gives NaN.
+ *   q, o   [B, Hq, d] contiguous, dtype as the pool's; 16-byte aligned.   lse  fp32 [B, Hq].
+ * Requires d = 64 or 128, Hq a multiple of Hkv.  Scores, softmax and sums in fp32.  The work is
+ * split evenly over the SMs whatever the lengths, and the parts are joined by a second launch.
+ */
+size_t gret_paged_attention_workspace_size(gret_dtype_t dtype, int Hq, int Hkv, int d);
+gret_status_t gret_paged_attention_decode(
+    const void* q, const int32_t* seq_lens, const int32_t* page_table, int64_t table_stride,
+    int max_pages, const void* k_pages, const void* v_pages, int64_t stride_page,
+    int64_t stride_tok, int64_t stride_head, int n_pages, int page_size, gret_dtype_t dtype,
+    float scale, int window, int B, int Hq, int Hkv, int d, void* o, float* lse, int32_t* status,
+    void* workspace, size_t workspace_bytes, gret_stream_t stream);
+
+/*
+ * Write new tokens' keys and values to their slots.  Packed: token i of the T tokens belongs to
+ * the row b with cu_seqlens[b] <= i < cu_seqlens[b + 1] (int32 [S + 1], device) and goes to
+ * position pos[b] + i - cu_seqlens[b]; tokens before the first and behind the last sequence are
+ * left alone.  cu_seqlens NULL: T = S, token i goes to position pos[i] of row i.  Rows with pos < 0
+ * are skipped (pos as gret_paged_resize gives it).
+ *   k, v   [T, Hkv, d], token i, head h at i * k_stride_tok + h * k_stride_head elements (v
+ *          likewise); 16-byte aligned.
+ */
+gret_status_t gret_paged_append(
+    const void* k, int64_t k_stride_tok, int64_t k_stride_head, const void* v,
+    int64_t v_stride_tok, int64_t v_stride_head, int64_t T, const int32_t* cu_seqlens,
+    const int32_t* pos, int S, const int32_t* page_table, int64_t table_stride, int max_pages,
+    void* k_pages, void* v_pages, int64_t stride_page, int64_t stride_tok, int64_t stride_head,
+    int n_pages, int page_size, gret_dtype_t dtype, int Hkv, int d, int32_t* status,
+    gret_stream_t stream);
+
+/*
+ * Change the sequences' lengths: seq_lens[s] becomes max(0, seq_lens[s] + delta[s]).
+ * A row that grows takes the pages it lacks, the lowest free ones, rows in order; pos[s] becomes
+ * its old length, where gret_paged_append puts the new tokens.  If its last page is partly filled
+ * and shared (ref > 1), the row first gets a page of its own in its place with a copy of the slots
+ * in use (copy on write).  A row that shrinks drops the pages past its new length (ref - 1, entry
+ * -1), and one shrunk to 0 has given everything back.  Pages dropped by a call can be taken from
+ * the next call on.  Not grown, and left as they are with pos = -1: a row past max_pages
+ * (TABLE_FULL), and a row that needs pages when those asked for by the rows up to it exceed the
+ * pages that are free (NO_PAGES).  pos = -1 for every row that does not grow.
+ */
+size_t gret_paged_resize_workspace_size(int S);
+gret_status_t gret_paged_resize(
+    const int32_t* delta, int32_t* seq_lens, int S, int32_t* page_table, int64_t table_stride,
+    int max_pages, int32_t* ref, void* k_pages, void* v_pages, int64_t stride_page,
+    int64_t stride_tok, int64_t stride_head, int n_pages, int page_size, gret_dtype_t dtype,
+    int Hkv, int d, int32_t* pos, int32_t* status, void* workspace, size_t workspace_bytes,
+    gret_stream_t stream);
+
+/*
+ * Let row dst[i] hold the pages of row src[i], for the n pairs: the table entries and the length
+ * are copied, ref + 1 each, no key or value moves.  dst[i] must be an empty row (length 0).  Refused
+ * (BAD_ROW), and without effect: a row out of range, a destination that is not empty or that an
+ * earlier pair names, a source that is a destination of any pair.
+ */
+gret_status_t gret_paged_fork(
+    const int32_t* src, const int32_t* dst, int n, int32_t* seq_lens, int S, int32_t* page_table,
+    int64_t table_stride, int max_pages, int32_t* ref, int n_pages, int page_size, int32_t* status,
+    gret_stream_t stream);
+
+/*
+ * Move the pages in use to the front of the pool.  With L pages in use (n_live[0] = L afterwards),
+ * the k-th page in use past index L moves to the k-th free page below L; ref and the table's
+ * entries follow.  Pages from L on are free afterwards, so that their memory can be given up.
+ */
+size_t gret_paged_compact_workspace_size(int n_pages);
+gret_status_t gret_paged_compact(
+    const int32_t* seq_lens, int S, int32_t* page_table, int64_t table_stride, int max_pages,
+    int32_t* ref, void* k_pages, void* v_pages, int64_t stride_page, int64_t stride_tok,
+    int64_t stride_head, int n_pages, int page_size, gret_dtype_t dtype, int Hkv, int d,
+    int32_t* n_live, int32_t* status, void* workspace, size_t workspace_bytes,
+    gret_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
