@@ -7,16 +7,33 @@
 // Parts of the keys give (m_i, l_i, a_i = sum e^(s_j - m_i) v_j), which join exactly:
 //     m = max m_i,  l = sum e^(m_i - m) l_i,  o = sum e^(m_i - m) a_i / l.
 //
+// Bound: HBM, 2 n d values a (sequence, kv head) read once, 2 G flops a value.  That little
+// arithmetic leaves the tensor cores idle for most of the time in any form, so the form is chosen
+// for the loads: every warp runs its own ring of cp.async tiles (KT keys and values of one head, 8
+// KB), two of them always in flight behind the one being worked on and across the borders of
+// sequences, with no barrier between warps but where a (sequence, head) ends; page-table entries
+// are read one tile ahead of that.  16-byte pieces gathered by lanes take any page size and any
+// stride, where a bulk copy would want one tensor map a layout and at least a page of tokens.
+//
+// bf16: keys are the M side of the product and the query heads of the group the N side (8 to 32,
+// padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows;
+// p is split into two bf16 parts (hi + lo = p up to 2^-16) because one part alone would put its
+// rounding of 2^-9 on every weight, and O^T = V^T P^T.  Both read their 16-bit tiles from shared
+// memory by ldmatrix, the accumulators stay in registers.  fp32: products in fp32 on the CUDA
+// cores, a lane a key for the scores and a lane four dimensions for the values.
+//
 // The work is cut into units of UNIT keys of one (sequence, kv head, group of query rows); the
 // units of the whole batch are dealt out evenly over the grid, in order, so that one long
 // sequence spreads over every SM and a ragged batch stays balanced without the host knowing the
 // lengths.  A block whose range ends inside a (sequence, head) writes its part to the workspace;
-// a second kernel joins the parts in block order, so that results do not depend on timing.
+// a second kernel joins the parts in block order, so that results do not depend on timing.  It is
+// launched as a dependent of the first one, whose end it waits for on the device.
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include "common.cuh"
 #include "paged.cuh"
+#include "sm100.cuh"
 
 namespace gret {
 
@@ -24,9 +41,14 @@ namespace {
 
 constexpr int NT = 128;
 constexpr int NW = NT / 32;
-constexpr int UNIT = 64;       // keys of one unit of work
-constexpr int ROWS = 8;        // query rows a block works on at a time
-constexpr int GRID = 148 * 4;
+constexpr int UNIT = 64;               // keys of one unit of work
+constexpr int S = 3;                   // tiles of a warp's ring
+constexpr int HALF = 4096;             // bytes of a tile's keys, and of its values
+constexpr int RING = S * 2 * HALF;
+constexpr int MAXROWS = 32;            // query rows a block works on at a time
+constexpr int BLOCKS_SM = 2;           // 2 x (4 rings of 24 KB + queries) fill an SM's 227 KB
+constexpr int GRID = 148 * BLOCKS_SM;
+constexpr int JOIN_NT = 128;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -38,10 +60,10 @@ struct Header {
 
 // Parts in the workspace: slot 2c is block c's head (the rest of a pair begun by an earlier
 // block), slot 2c + 1 its tail (a pair that a later block goes on with).
-template <int D>
+template <int R, int D>
 struct Part {
-    float m[ROWS], l[ROWS];      // m in units of log2
-    float a[ROWS][D];
+    float m[R], l[R];            // m in units of log2
+    float a[R][D];
 };
 
 struct Params {
@@ -50,7 +72,7 @@ struct Params {
     PagedTable table;
     PagedPool pool;
     float scale_log2;
-    int window, Hq, G, QG;       // query heads a kv head; groups of ROWS of them
+    int window, Hq, G, QG;       // query heads a kv head; groups of rows of them
     void* o;
     float* lse;
     int32_t* status;
@@ -58,50 +80,403 @@ struct Params {
     void* parts;
 };
 
-// Keys [first, len) of sequence b.
-__device__ __forceinline__ void key_range(const Params& p, int b, int64_t& first, int64_t& len) {
-    const int64_t cap = (int64_t)p.table.max_pages << p.pool.page_shift;
-    len = p.lens[b];
-    if (len < 0 || len > cap) {
-        paged_flag(p.status, GRET_PAGED_BAD_LENGTH);
-        len = len < 0 ? 0 : cap;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 bytes to shared memory, zeros where `bytes` is 0 (the source is then not read).
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The arithmetic on a tile of KT keys and values, by one warp.  The tile's row r begins at r * ROWB
+// and its 16-byte piece c lies in place c ^ (r & 7), so that reads of one piece of 8 rows, and of
+// one whole row, touch every bank once.
+
+template <int D_, int NQ>
+struct Bf16Math {
+    using T = __nv_bfloat16;
+    static constexpr int D = D_, ROWS = 8 * NQ, ROWB = D * 2, KT = HALF / ROWB;
+    static constexpr int QROW = ROWB + 16;           // 16 more bytes: rows begin in other banks
+    static constexpr int QBYTES = ROWS * QROW, SCRATCH = 0, NPASS = NQ;
+
+    uint32_t qf[NQ][D / 16][2];
+    float m[NQ][2], l[NQ][2], acc[NQ][D / 16][4];
+
+    __device__ static __forceinline__ int q_place(int r, int c) { return r * QROW + c * 16; }
+
+    __device__ __forceinline__ void begin(const unsigned char* qs, unsigned char*, int lane) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const unsigned char* at = qs + (8 * i + lane / 4) * QROW + 32 * k + 4 * (lane & 3);
+                qf[i][k][0] = *reinterpret_cast<const uint32_t*>(at);
+                qf[i][k][1] = *reinterpret_cast<const uint32_t*>(at + 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][k][e] = 0.f;
+            }
+            m[i][0] = m[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.f;
+        }
     }
-    first = p.window > 0 && len > p.window ? len - p.window : 0;
+
+    // Bit r of `ok`: key r counts.
+    __device__ __forceinline__ void tile(const unsigned char* ks, const unsigned char* vs,
+                                         const unsigned char*, unsigned char*, unsigned ok,
+                                         float scale, int lane) {
+        const uint32_t kb = sm100::smem_u32(ks), vb = sm100::smem_u32(vs);
+#pragma unroll
+        for (int j = 0; j < KT; j += 16) {
+            float s[NQ][4];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t a[4];
+                const int r = j + (lane & 15), c = 2 * k + (lane >> 4);
+                ldmatrix4(a, kb + r * ROWB + ((c ^ (r & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) mma_16x8x16(s[i], a, qf[i][k][0], qf[i][k][1]);
+            }
+            // s[i]: key lane/4 (0, 1) and lane/4 + 8 (2, 3), queries 8i + 2 (lane & 3) and the next
+            const bool ok0 = ok >> (j + lane / 4) & 1, ok1 = ok >> (j + 8 + lane / 4) & 1;
+            uint32_t hi[NQ][2], lo[NQ][2];
+            bool up = false;
+            float mn[NQ][2];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    s[i][e] = ok0 ? s[i][e] * scale : -INFINITY;
+                    s[i][2 + e] = ok1 ? s[i][2 + e] * scale : -INFINITY;
+                    float x = fmaxf(s[i][e], s[i][2 + e]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+                    mn[i][e] = fmaxf(m[i][e], x);
+                    up |= mn[i][e] != m[i][e];
+                }
+            if (__any_sync(~0u, up)) {
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    float f[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // m = -inf: nothing summed up so far, whatever the factor
+                        f[e] = m[i][e] == -INFINITY ? 0.f : ex2(m[i][e] - mn[i][e]);
+                        l[i][e] *= f[e];
+                        m[i][e] = mn[i][e];
+                    }
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[i][k][e] *= f[e & 1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                float p[4], x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float base = m[i][e & 1] == -INFINITY ? 0.f : m[i][e & 1];
+                    p[e] = ex2(s[i][e] - base);
+                    l[i][e & 1] += p[e];
+                    // hi: p cut off after 8 bits.  lo: the rest, and 2^-20 p more, so that it is
+                    // not 0 where p is a bf16 value (0 times an infinite value would be NaN)
+                    const float h = __uint_as_float(__float_as_uint(p[e]) & 0xffff0000u);
+                    x[e] = fmaf(p[e], 0x1p-20f, p[e] - h);
+                }
+                hi[i][0] = transpose8x8(__byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]),
+                                                    0x7632));
+                hi[i][1] = transpose8x8(__byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]),
+                                                    0x7632));
+                lo[i][0] = transpose8x8(pack_bf16(x[0], x[1]));
+                lo[i][1] = transpose8x8(pack_bf16(x[2], x[3]));
+            }
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t a[4];
+                const int r = j + (lane & 7) + (lane >> 4) * 8, c = 2 * k + (lane >> 3 & 1);
+                ldmatrix4_trans(a, vb + r * ROWB + ((c ^ (r & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    mma_16x8x16(acc[i][k], a, hi[i][0], hi[i][1]);
+                    mma_16x8x16(acc[i][k], a, lo[i][0], lo[i][1]);
+                }
+            }
+        }
+    }
+
+    // The warp's maxima and sums of all rows.
+    __device__ __forceinline__ void end(float* wm, float* wl, int lane) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(~0u, l[i][e], o);
+                if (lane < 4) {
+                    wm[8 * i + 2 * lane + e] = m[i][e];
+                    wl[8 * i + 2 * lane + e] = l[i][e];
+                }
+            }
+    }
+
+    // The sums of 8 rows of values, to rows of D + 4 (so that the lanes' banks differ).
+    __device__ __forceinline__ void put(int pass, float* to, int lane) {
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+            if (i == pass)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        to[(2 * (lane & 3) + (e & 1)) * (D + 4) + 16 * k + lane / 4 + (e >> 1) * 8] =
+                            acc[i][k][e];
+    }
+};
+
+template <int D_, int R>
+struct F32Math {
+    using T = float;
+    static constexpr int D = D_, ROWS = R, ROWB = D * 4, KT = HALF / ROWB;
+    static constexpr int CPR = ROWB / 16, KI = 32 / CPR;   // pieces a row; rows a warp-wide read
+    // a query row in parts of 32 dimensions, 16 bytes between them: the parts begin in other banks
+    static constexpr int QROW = D / 32 * 144;
+    static constexpr int QBYTES = R * QROW, SCRATCH = KT * R * 4, NPASS = 1;
+
+    float m[R], l[R], acc[R][4];
+
+    __device__ static __forceinline__ int q_place(int r, int c) {
+        return r * QROW + c / 8 * 144 + c % 8 * 16;
+    }
+
+    __device__ __forceinline__ void begin(const unsigned char*, unsigned char*, int) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[r][e] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void tile(const unsigned char* ks, const unsigned char* vs,
+                                         const unsigned char* qs, unsigned char* scratch,
+                                         unsigned ok, float scale, int lane) {
+        const int key = lane % KT, part = lane / KT;       // this lane's 32 of the D dimensions
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float4 k = *reinterpret_cast<const float4*>(
+                ks + key * ROWB + (((part * 8 + c) ^ (key & 7)) << 4));
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 q =
+                    *reinterpret_cast<const float4*>(qs + r * QROW + part * 144 + c * 16);
+                s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+            }
+        }
+        const bool okk = ok >> key & 1;
+        float mn[R];
+        bool up = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int o = KT; o < 32; o <<= 1) s[r] += __shfl_xor_sync(~0u, s[r], o);
+            s[r] = okk ? s[r] * scale : -INFINITY;
+            float x = s[r];
+#pragma unroll
+            for (int o = 1; o < KT; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+            mn[r] = fmaxf(m[r], x);
+            up |= mn[r] != m[r];
+        }
+        if (__any_sync(~0u, up)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn[r]);
+                l[r] *= f;
+                m[r] = mn[r];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][e] *= f;
+            }
+        }
+        float* pk = reinterpret_cast<float*>(scratch);     // [KT][R]
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] = ex2(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+            l[r] += s[r];
+        }
+        if (part == 0)
+#pragma unroll
+            for (int r = 0; r < R; r += 4)
+                *reinterpret_cast<float4*>(pk + key * R + r) =
+                    make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+        __syncwarp();
+        const int c = lane % CPR;
+#pragma unroll
+        for (int j = 0; j < KT; j += KI) {
+            const int row = j + lane / CPR;
+            const float4 v =
+                *reinterpret_cast<const float4*>(vs + row * ROWB + ((c ^ (row & 7)) << 4));
+#pragma unroll
+            for (int r = 0; r < R; r += 4) {
+                const float4 p = *reinterpret_cast<const float4*>(pk + row * R + r);
+                const float pr[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[r + e][0] = fmaf(pr[e], v.x, acc[r + e][0]);
+                    acc[r + e][1] = fmaf(pr[e], v.y, acc[r + e][1]);
+                    acc[r + e][2] = fmaf(pr[e], v.z, acc[r + e][2]);
+                    acc[r + e][3] = fmaf(pr[e], v.w, acc[r + e][3]);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void end(float* wm, float* wl, int lane) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int o = 1; o < KT; o <<= 1) l[r] += __shfl_xor_sync(~0u, l[r], o);
+            if (lane == 0) {
+                wm[r] = m[r];
+                wl[r] = l[r];
+            }
+        }
+    }
+
+    __device__ __forceinline__ void put(int, float* to, int lane) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (KI == 2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][e] += __shfl_xor_sync(~0u, acc[r][e], 16);
+            if (lane < CPR)
+                *reinterpret_cast<float4*>(to + r * (D + 4) + 4 * lane) =
+                    make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+        }
+    }
+};
+
+// Keys [first, len) of sequence b.
+__device__ __forceinline__ void key_range(const Params& p, int b, uint32_t& first, uint32_t& len) {
+    const int64_t cap = (int64_t)p.table.max_pages << p.pool.page_shift;
+    const int n = p.lens[b];
+    len = n;
+    if (n < 0 || n > cap) {
+        paged_flag(p.status, GRET_PAGED_BAD_LENGTH);
+        len = n < 0 ? 0 : (uint32_t)cap;
+    }
+    first = p.window > 0 && len > (uint32_t)p.window ? len - p.window : 0;
 }
 
-__device__ __forceinline__ int64_t units_of(const Params& p, int b) {
-    int64_t first, len;
+__device__ __forceinline__ int units_between(uint32_t first, uint32_t len) {
+    return (int)((len - first + UNIT - 1) / UNIT);
+}
+
+__device__ __forceinline__ int units_of(const Params& p, int b) {
+    uint32_t first, len;
     key_range(p, b, first, len);
-    return (len - first + UNIT - 1) / UNIT;
+    return units_between(first, len);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(NT) paged_attn_kernel(const Params p) {
-    constexpr int E = D / 32;    // dimensions a lane holds
-    __shared__ float qs[ROWS][D];
-    __shared__ float wm[NW][ROWS], wl[NW][ROWS], wa[NW][ROWS][D];
+// A stretch of one pair's units that a block works on: units [t0, t1) of nu.
+struct Segment {
+    int64_t u;                   // of the whole batch's units, the one t0 stands for
+    uint32_t first, len;
+    int b, pr, nu, t0, t1;
+
+    __device__ __forceinline__ uint32_t key0() const { return first + (uint32_t)t0 * UNIT; }
+    __device__ __forceinline__ uint32_t key1() const {
+        return t1 == nu ? len : first + (uint32_t)t1 * UNIT;
+    }
+    // To the next one of a block whose units end before u1.
+    __device__ __forceinline__ bool next(const Params& p, int64_t u1) {
+        u += t1 - t0;
+        if (u >= u1) return false;
+        t0 = 0;                  // only a block's last segment ends inside its pair
+        if (++pr == p.pool.H * p.QG) {
+            pr = 0;
+            do {
+                if (++b == p.table.S) return false;
+                key_range(p, b, first, len);
+            } while (len == first);
+            nu = units_between(first, len);
+        }
+        t1 = (int)min((int64_t)nu, u1 - u);
+        return true;
+    }
+};
+
+template <class M>
+__global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params p) {
+    using T = typename M::T;
+    constexpr int D = M::D, KT = M::KT, ROWB = M::ROWB, CPR = ROWB / 16;
+    constexpr int QC = (M::ROWS * CPR + NT - 1) / NT;      // pieces of the queries a thread moves
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float wm[NW][M::ROWS], wl[NW][M::ROWS];
+    __shared__ const float* wput[NW];
     __shared__ int64_t scan[NW], start_unit;
     __shared__ int start_b;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned char* ring = smem + warp * RING;
+    unsigned char* qs = smem + NW * RING;
+    unsigned char* scratch = qs + M::QBYTES + warp * M::SCRATCH;
     const int B = p.table.S, pairs_b = p.pool.H * p.QG;
-
-    // sequences without keys: zeros
-    for (int b = blockIdx.x; b < B; b += gridDim.x)
-        if (units_of(p, b) == 0) {
-            for (int i = tid; i < p.Hq * D; i += NT)
-                static_cast<T*>(p.o)[(int64_t)b * p.Hq * D + i] = from_f32<T>(0.f);
-            if (p.lse)
-                for (int i = tid; i < p.Hq; i += NT) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
-        }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // this block's range of units, [u0, u1) of U.  With fewer units than blocks, the first U blocks
     // take one each: a pair's parts lie in consecutive blocks
     const int per = (B + NT - 1) / NT;
     int64_t mine = 0;
-    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b) mine += units_of(p, b) * pairs_b;
+    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b)
+        mine += (int64_t)units_of(p, b) * pairs_b;
     int64_t incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        const int64_t x = __shfl_up_sync(~0u, incl, o);
         if (lane >= o) incl += x;
     }
     if (lane == 31) scan[warp] = incl;
@@ -121,170 +496,303 @@ __global__ void __launch_bounds__(NT) paged_attn_kernel(const Params p) {
         int b = tid * per;
         int64_t at = before;
         for (;; ++b) {
-            const int64_t x = units_of(p, b) * pairs_b;
-            if (u0 < at + x) break;
+            const int64_t x = (int64_t)units_of(p, b) * pairs_b;
+            if (u0 < at + x || b + 1 == B) break;
             at += x;
         }
         start_b = b;
         start_unit = at;
     }
     __syncthreads();
-    int b = start_b;
-    int64_t first, len;
-    key_range(p, b, first, len);
-    int64_t nu = (len - first + UNIT - 1) / UNIT;
-    int pr = (int)((u0 - start_unit) / nu);              // pair within the sequence
-    int64_t t0 = (u0 - start_unit) % nu;                 // first unit of the segment in its pair
-    int64_t u = u0;
+    Segment seg;
+    seg.b = start_b;
+    key_range(p, seg.b, seg.first, seg.len);
+    seg.nu = units_between(seg.first, seg.len);
+    seg.u = u0;
+    seg.pr = (int)((u0 - start_unit) / seg.nu);
+    seg.t0 = (int)((u0 - start_unit) % seg.nu);
+    seg.t1 = (int)min((int64_t)seg.nu, seg.t0 + (u1 - u0));
     Header header = {-1, 0};
-    const int page_mask = (1 << p.pool.page_shift) - 1;
 
-    while (u < u1) {
-        const int64_t t1 = min(nu, t0 + (u1 - u));
-        const int h = pr / p.QG, qg = pr % p.QG;
-        const int rows = min(ROWS, p.G - qg * ROWS);
-        const int64_t head0 = (int64_t)b * p.Hq + h * p.G + qg * ROWS;   // first query row
-        __syncthreads();
-        for (int i = tid; i < ROWS * D; i += NT)
-            qs[i / D][i % D] = i / D < rows
-                                   ? to_f32(static_cast<const T*>(p.q)[head0 * D + i]) * p.scale_log2
-                                   : 0.f;
-        __syncthreads();
-        float m[ROWS], l[ROWS], acc[ROWS][E];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
+    // The tile to load next.  Its page-table entries are read when it becomes that, a whole tile's
+    // work before they are needed.
+    Segment ls = seg;
+    uint32_t at = ls.key0() + warp * KT, end = ls.key1();
+    bool more = true;
+    int id = 0;
+    const int page_shift = p.pool.page_shift;
+    auto look_up = [&]() {
+        while (more && at >= end) {
+            more = ls.next(p, u1);
+            at = ls.key0() + warp * KT;
+            end = ls.key1();
         }
-        const int64_t key1 = min(len, first + t1 * UNIT);
-        for (int64_t j = first + t0 * UNIT + warp; j < key1; j += NW) {
-            const int id = p.table.entries[b * p.table.stride + (j >> p.pool.page_shift)];
-            if ((unsigned)id >= (unsigned)p.pool.n_pages) {
-                if (lane == 0) paged_flag(p.status, GRET_PAGED_BAD_PAGE);
-                continue;
-            }
-            const int64_t off = id * p.pool.sp + (j & page_mask) * p.pool.st + h * p.pool.sh;
-            const T* kr = reinterpret_cast<const T*>(p.pool.k + off);
-            const T* vr = reinterpret_cast<const T*>(p.pool.v + off);
-            float kf[E], vf[E];
+        if (more && lane < KT && at + lane < end)
+            id = p.table.entries[ls.b * p.table.stride + ((at + lane) >> page_shift)];
+    };
+    // Load it, and go on to the next: a bit for every key that counts.
+    auto load = [&](int stage) {
+        unsigned ok = 0;
+        if (more) {
+            const bool in = lane < KT && at + lane < end;
+            const bool good = in && (unsigned)id < (unsigned)p.pool.n_pages;
+            if (in && !good) paged_flag(p.status, GRET_PAGED_BAD_PAGE);
+            ok = __ballot_sync(~0u, good);
+            const int64_t off = !good ? 0
+                                      : id * p.pool.sp +
+                                            ((at + lane) & ((1u << page_shift) - 1)) * p.pool.st +
+                                            ls.pr / p.QG * p.pool.sh;
+            const uint32_t to = sm100::smem_u32(ring + stage * 2 * HALF);
+            const int c = lane % CPR;
+            at += NW * KT;
+            look_up();
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                kf[e] = to_f32(kr[lane + 32 * e]);
-                vf[e] = to_f32(vr[lane + 32 * e]);
-            }
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
-                float s = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) s = fmaf(qs[r][lane + 32 * e], kf[e], s);
-                for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                const float mn = fmaxf(m[r], s);
-                const float base = mn == -INFINITY ? 0.f : mn;
-                const float corr = exp2f(m[r] - base), pj = exp2f(s - base);
-                l[r] = l[r] * corr + pj;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[r][e] = acc[r][e] * corr + pj * vf[e];
-                m[r] = mn;
+            for (int i = 0; i < KT * CPR / 32; ++i) {
+                const int r = i * (32 / CPR) + lane / CPR;
+                const int64_t o = __shfl_sync(~0u, off, r) + c * 16;
+                const uint32_t dst = to + r * ROWB + ((c ^ (r & 7)) << 4);
+                const uint32_t bytes = ok >> r & 1 ? 16 : 0;
+                cp_async_16_or_zero(dst, p.pool.k + o, bytes);
+                cp_async_16_or_zero(dst + HALF, p.pool.v + o, bytes);
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return ok;
+    };
+    unsigned ok[S];
+    look_up();
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (lane == 0) {
-                wm[warp][r] = m[r];
-                wl[warp][r] = l[r];
-            }
+    for (int i = 0; i < S - 1; ++i) ok[i] = load(i);
+    int stage = 0;
+
+    // A segment's queries: read one segment ahead, put into shared memory when it begins.
+    uint4 qn[QC];
+    auto read_q = [&](const Segment& s) {
+        const int h = s.pr / p.QG, qg = s.pr % p.QG;
+        const int rows = min(M::ROWS, p.G - qg * M::ROWS);
+        const T* q = static_cast<const T*>(p.q) +
+                     ((int64_t)s.b * p.Hq + h * p.G + qg * M::ROWS) * D;
 #pragma unroll
-            for (int e = 0; e < E; ++e) wa[warp][r][lane + 32 * e] = acc[r][e];
+        for (int i = 0; i < QC; ++i) {
+            const int x = tid + i * NT;
+            qn[i] = x < rows * CPR ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
         }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == nu;
-        Part<D>* part = static_cast<Part<D>*>(p.parts) + 2 * blockIdx.x + (t0 == 0);
-        if (!whole && t0 == 0) {
+    };
+    auto put_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            const int x = tid + i * NT;
+            if (x < M::ROWS * CPR)
+                *reinterpret_cast<uint4*>(qs + M::q_place(x / CPR, x % CPR)) = qn[i];
+        }
+    };
+    read_q(seg);
+    put_q();
+    __syncthreads();
+
+    M math;
+    for (bool go = true; go;) {
+        Segment nx = seg;
+        go = nx.next(p, u1);
+        if (go) read_q(nx);
+        math.begin(qs, scratch, lane);
+        const uint32_t key1 = seg.key1();
+        for (uint32_t k = seg.key0() + warp * KT; k < key1; k += NW * KT) {
+            ok[S - 1] = load(stage == 0 ? S - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+            __syncwarp();
+            const unsigned char* t = ring + stage * 2 * HALF;
+            math.tile(t, t + HALF, qs, scratch, ok[0], p.scale_log2, lane);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) ok[i] = ok[i + 1];
+            stage = stage == S - 1 ? 0 : stage + 1;
+        }
+        // join the warps' parts, through the ring's one stage that no load is under way to
+        const int h = seg.pr / p.QG, qg = seg.pr % p.QG;
+        const int rows = min(M::ROWS, p.G - qg * M::ROWS);
+        const int64_t head0 = (int64_t)seg.b * p.Hq + h * p.G + qg * M::ROWS;   // first query row
+        const bool whole = seg.t0 == 0 && seg.t1 == seg.nu;
+        Part<M::ROWS, D>* part =
+            static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * blockIdx.x + (seg.t0 == 0);
+        if (!whole && seg.t0 == 0) {
             // the block that holds unit x is the largest c with floor(c U / blocks) <= x
-            const int64_t x = u + nu - 1;
-            header.pair = (b * p.pool.H + h) * p.QG + qg;
+            const int64_t x = seg.u + seg.nu - 1;
+            header.pair = (seg.b * p.pool.H + h) * p.QG + qg;
             header.parts = (int)(((x + 1) * blocks - 1) / U - blockIdx.x) + 1;
         }
-        for (int i = tid; i < rows * D; i += NT) {
-            const int r = i / D, e = i % D;
-            float M = -INFINITY;
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w][r]);
-            const float base = M == -INFINITY ? 0.f : M;
-            float a = 0.f, z = 0.f;
-            for (int w = 0; w < NW; ++w) {
-                const float f = exp2f(wm[w][r] - base);
-                a += wa[w][r][e] * f;
-                z += wl[w][r] * f;
-            }
-            if (whole) {
-                static_cast<T*>(p.o)[head0 * D + i] = from_f32<T>(a / z);
-                if (p.lse && e == 0) p.lse[head0 + r] = (M + log2f(z)) * LN2;
-            } else {
-                part->a[r][e] = a;
-                if (e == 0) {
-                    part->m[r] = M;
-                    part->l[r] = z;
+        float* mine_put =
+            reinterpret_cast<float*>(ring + (stage == 0 ? S - 1 : stage - 1) * 2 * HALF);
+        if (lane == 0) wput[warp] = mine_put;
+        math.end(wm[warp], wl[warp], lane);
+#pragma unroll
+        for (int pass = 0; pass < M::NPASS; ++pass) {
+            constexpr int PR = M::ROWS / M::NPASS;         // rows of a pass
+            math.put(pass, mine_put, lane);
+            __syncthreads();
+            if (pass == 0 && go) put_q();
+            for (int i = tid; i < PR * D / 4; i += NT) {
+                const int r = i / (D / 4), e = i % (D / 4) * 4, row = pass * PR + r;
+                if (row >= rows) break;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w][row]);
+                const float base = mx == -INFINITY ? 0.f : mx;
+                float a[4] = {}, z = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const float f = ex2(wm[w][row] - base);
+                    const float4 x = *reinterpret_cast<const float4*>(wput[w] + r * (D + 4) + e);
+                    a[0] += x.x * f;
+                    a[1] += x.y * f;
+                    a[2] += x.z * f;
+                    a[3] += x.w * f;
+                    z += wl[w][row] * f;
+                }
+                if (whole) {
+                    T* o = static_cast<T*>(p.o) + (head0 + row) * D + e;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[x] = from_f32<T>(a[x] / z);
+                    if (p.lse && e == 0) p.lse[head0 + row] = (mx + log2f(z)) * LN2;
+                } else {
+                    *reinterpret_cast<float4*>(&part->a[row][e]) =
+                        make_float4(a[0], a[1], a[2], a[3]);
+                    if (e == 0) {
+                        part->m[row] = mx;
+                        part->l[row] = z;
+                    }
                 }
             }
+            __syncthreads();
         }
-        u += t1 - t0;
-        t0 = 0;
-        if (t1 == nu && ++pr == pairs_b && u < u1) {
-            pr = 0;
-            do {
-                ++b;
-                key_range(p, b, first, len);
-            } while (len == first);
-            nu = (len - first + UNIT - 1) / UNIT;
-        }
+        seg = nx;
     }
     if (tid == 0) p.headers[blockIdx.x] = header;
 }
 
-// Block c joins the parts of the pair that block c of the kernel above began and did not finish.
-template <typename T, int D>
-__global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
-    const Header hd = p.headers[blockIdx.x];
+// Block (c, r) joins row r of the parts of the pair that block c of the kernel above began and
+// did not finish: a warp a quarter of the parts, a lane D / 32 dimensions.
+template <class M>
+__global__ void __launch_bounds__(JOIN_NT) paged_join_kernel(const Params p) {
+    using T = typename M::T;
+    constexpr int D = M::D, E = D / 32, JW = JOIN_NT / 32, UN = 4;
+    __shared__ float w[GRID];            // the parts' maxima, then their weights
+    __shared__ float sums[JW][D], red[JW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
+    // sequences without keys: zeros, with nothing to wait for
+    for (int b = blockIdx.x; b < p.table.S; b += GRID)
+        if (units_of(p, b) == 0)
+            for (int i = r; i < p.Hq; i += gridDim.y) {
+                for (int e = tid; e < D; e += JOIN_NT)
+                    static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * D + e] = from_f32<T>(0.f);
+                if (p.lse && tid == 0) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
+            }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x;
+    const Header hd = p.headers[c];
     if (hd.pair < 0) return;
     const int qg = hd.pair % p.QG;
-    const int64_t bh = hd.pair / p.QG;
-    const int rows = min(ROWS, p.G - qg * ROWS);
-    const int64_t head0 = bh * p.G + qg * ROWS;
-    const Part<D>* parts = static_cast<const Part<D>*>(p.parts);
-    const int c = blockIdx.x;
-    for (int i = threadIdx.x; i < rows * D; i += NT) {
-        const int r = i / D, e = i % D;
-        float M = -INFINITY;
-        for (int k = 0; k < hd.parts; ++k) M = fmaxf(M, parts[2 * (c + k) + (k == 0)].m[r]);
-        const float base = M == -INFINITY ? 0.f : M;
-        float a = 0.f, z = 0.f;
-        for (int k = 0; k < hd.parts; ++k) {
-            const Part<D>& x = parts[2 * (c + k) + (k == 0)];
-            const float f = exp2f(x.m[r] - base);
-            a += x.a[r][e] * f;
-            z += x.l[r] * f;
-        }
-        static_cast<T*>(p.o)[head0 * D + i] = from_f32<T>(a / z);
-        if (p.lse && e == 0) p.lse[head0 + r] = (M + log2f(z)) * LN2;
+    if (r >= min(M::ROWS, p.G - qg * M::ROWS)) return;
+    const int64_t head = (int64_t)(hd.pair / p.QG) * p.G + qg * M::ROWS + r;
+    const Part<M::ROWS, D>* parts = static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c;
+    // part k: the tail of block c, then the heads of those that follow
+    float mx = -INFINITY;
+    for (int k = tid; k < hd.parts; k += JOIN_NT) {
+        w[k] = parts[2 * k + (k == 0)].m[r];
+        mx = fmaxf(mx, w[k]);
     }
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+    if (lane == 0) red[warp] = mx;
+    __syncthreads();
+    for (int i = 0; i < JW; ++i) mx = fmaxf(mx, red[i]);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float z = 0.f;
+    for (int k = tid; k < hd.parts; k += JOIN_NT) {
+        const float f = ex2(w[k] - base);
+        w[k] = f;
+        z += f * parts[2 * k + (k == 0)].l[r];
+    }
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
+    __syncthreads();
+    if (lane == 0) red[warp] = z;
+    float a[E] = {};
+    for (int k0 = warp; k0 < hd.parts; k0 += JW * UN) {
+        float x[UN][E];
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int k = k0 + i * JW;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[i][e] = k < hd.parts ? parts[2 * k + (k == 0)].a[r][lane + 32 * e] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int k = k0 + i * JW;
+            const float f = k < hd.parts ? w[k] : 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] = fmaf(f, x[i][e], a[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = a[e];
+    __syncthreads();
+    z = 0.f;
+    for (int i = 0; i < JW; ++i) z += red[i];
+    for (int e = tid; e < D; e += JOIN_NT) {
+        float x = 0.f;
+        for (int i = 0; i < JW; ++i) x += sums[i][e];
+        static_cast<T*>(p.o)[head * D + e] = from_f32<T>(x / z);
+    }
+    if (p.lse && tid == 0) p.lse[head] = (mx + log2f(z)) * LN2;
 }
 
-template <typename T, int D>
-cudaError_t launch(const Params& p, cudaStream_t stream) {
-    paged_attn_kernel<T, D><<<GRID, NT, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+template <class M>
+cudaError_t launch(Params& p, cudaStream_t stream) {
+    constexpr int smem = NW * (RING + M::SCRATCH) + M::QBYTES;
+    p.QG = (p.G + M::ROWS - 1) / M::ROWS;
+    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<M>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    paged_join_kernel<T, D><<<GRID, NT, 0, stream>>>(p);
-    return cudaGetLastError();
+    paged_attn_kernel<M><<<GRID, NT, smem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(GRID, M::ROWS < p.G ? M::ROWS : p.G);
+    cfg.blockDim = dim3(JOIN_NT);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<M>, static_cast<const Params&>(p));
+}
+
+// Query rows a block works on at a time: all G heads of a group where they fit, else the fewest
+// equal passes over the keys (each pass reads them again).
+int rows_of(bool bf16, int G) {
+    if (!bf16) return G <= 4 ? 4 : 8;
+    const int tiles = (G + 7) / 8, passes = (tiles + MAXROWS / 8 - 1) / (MAXROWS / 8);
+    return (tiles + passes - 1) / passes * 8;
+}
+
+template <int D>
+cudaError_t launch_d(bool bf16, int rows, Params& p, cudaStream_t stream) {
+    if (!bf16)
+        return rows == 4 ? launch<F32Math<D, 4>>(p, stream) : launch<F32Math<D, 8>>(p, stream);
+    switch (rows) {
+        case 8: return launch<Bf16Math<D, 1>>(p, stream);
+        case 16: return launch<Bf16Math<D, 2>>(p, stream);
+        case 24: return launch<Bf16Math<D, 3>>(p, stream);
+        default: return launch<Bf16Math<D, 4>>(p, stream);
+    }
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(bool, int, int, int d) {
+size_t paged_attn_workspace(bool bf16, int Hq, int Hkv, int d) {
     const size_t head = (GRID * sizeof(Header) + 255) / 256 * 256;
-    return head + 2 * GRID * (d == 64 ? sizeof(Part<64>) : sizeof(Part<128>));
+    return head + (size_t)2 * GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
@@ -297,16 +805,13 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.window = a.window;
     p.Hq = a.Hq;
     p.G = a.Hq / a.pool.H;
-    p.QG = (p.G + ROWS - 1) / ROWS;
     p.o = a.o;
     p.lse = a.lse;
     p.status = a.status;
     p.headers = static_cast<Header*>(a.workspace);
     p.parts = static_cast<unsigned char*>(a.workspace) + (GRID * sizeof(Header) + 255) / 256 * 256;
-    if (a.bf16)
-        return a.d == 64 ? launch<__nv_bfloat16, 64>(p, stream)
-                         : launch<__nv_bfloat16, 128>(p, stream);
-    return a.d == 64 ? launch<float, 64>(p, stream) : launch<float, 128>(p, stream);
+    const int rows = rows_of(a.bf16, p.G);
+    return a.d == 64 ? launch_d<64>(a.bf16, rows, p, stream) : launch_d<128>(a.bf16, rows, p, stream);
 }
 
 }  // namespace gret
