@@ -48,15 +48,8 @@ constexpr int RING = S * 2 * HALF;
 constexpr int MAXROWS = 32;            // query rows a block works on at a time
 constexpr int BLOCKS_SM = 2;           // 2 x (4 rings of 24 KB + queries) fill an SM's 227 KB
 constexpr int GRID = 148 * BLOCKS_SM;
-constexpr int JOIN_NT = 128;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-
-// What the join needs of block c: the pair whose first part block c holds (-1: none), and the
-// number of blocks that hold parts of it (block c's tail slot, then the head slots of the next).
-struct Header {
-    int32_t pair, parts;
-};
 
 // Parts in the workspace: slot 2c is block c's head (the rest of a pair begun by an earlier
 // block), slot 2c + 1 its tail (a pair that a later block goes on with).
@@ -76,7 +69,6 @@ struct Params {
     void* o;
     float* lse;
     int32_t* status;
-    Header* headers;
     void* parts;
 };
 
@@ -451,6 +443,71 @@ struct Segment {
     }
 };
 
+// How the batch's U units are dealt: `blocks` blocks, block c has units [U c / blocks,
+// U (c + 1) / blocks).  With fewer units than blocks, the first U blocks take one each: a pair's
+// parts lie in consecutive blocks.
+struct Deal {
+    int64_t U, blocks;
+
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return U * c / blocks; }
+    // The block that holds unit x is the largest c with floor(c U / blocks) <= x.
+    __device__ __forceinline__ int block_of(int64_t x) const {
+        return (int)(((x + 1) * blocks - 1) / U);
+    }
+};
+
+struct DealSmem {
+    int64_t scan[NT / 32], unit;
+    int b;
+};
+
+// The deal, and the place of the first (`last`: the last) unit of block c: its sequence b, and
+// the first unit of that.  Called by all NT threads; without units for block c, b = -1.
+__device__ __forceinline__ Deal deal_of(const Params& p, int c, bool last, DealSmem& sm, int& b,
+                                        int64_t& unit) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int B = p.table.S, pairs_b = p.pool.H * p.QG, per = (B + NT - 1) / NT;
+    const int b1 = min(B, (tid + 1) * per);
+    int64_t mine = 0;
+    for (int i = tid * per; i < b1; ++i) mine += (int64_t)units_of(p, i) * pairs_b;
+    int64_t incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    __syncthreads();
+    Deal d;
+    d.U = 0;
+    int64_t before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) before += sm.scan[w];
+        d.U += sm.scan[w];
+    }
+    d.blocks = min(d.U, (int64_t)GRID);
+    b = -1;
+    unit = 0;
+    if (c >= d.blocks) return d;
+    const int64_t u = last ? d.begin(c + 1) - 1 : d.begin(c);
+    if (before <= u && u < before + mine) {
+        int64_t at = before;
+        for (int i = tid * per; i < b1; ++i) {
+            const int64_t x = (int64_t)units_of(p, i) * pairs_b;
+            if (u < at + x) {
+                sm.b = i;
+                sm.unit = at;
+                break;
+            }
+            at += x;
+        }
+    }
+    __syncthreads();
+    b = sm.b;
+    unit = sm.unit;
+    return d;
+}
+
 template <class M>
 __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params p) {
     using T = typename M::T;
@@ -459,60 +516,23 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float wm[NW][M::ROWS], wl[NW][M::ROWS];
     __shared__ const float* wput[NW];
-    __shared__ int64_t scan[NW], start_unit;
-    __shared__ int start_b;
+    __shared__ DealSmem deal_smem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     unsigned char* ring = smem + warp * RING;
     unsigned char* qs = smem + NW * RING;
     unsigned char* scratch = qs + M::QBYTES + warp * M::SCRATCH;
-    const int B = p.table.S, pairs_b = p.pool.H * p.QG;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
-    // this block's range of units, [u0, u1) of U.  With fewer units than blocks, the first U blocks
-    // take one each: a pair's parts lie in consecutive blocks
-    const int per = (B + NT - 1) / NT;
-    int64_t mine = 0;
-    for (int b = tid * per; b < min(B, (tid + 1) * per); ++b)
-        mine += (int64_t)units_of(p, b) * pairs_b;
-    int64_t incl = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += x;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t U = 0, before = incl - mine;
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += scan[w];
-        U += scan[w];
-    }
-    const int64_t blocks = min(U, (int64_t)gridDim.x);
-    if (blockIdx.x >= blocks) {
-        if (tid == 0) p.headers[blockIdx.x] = {-1, 0};
-        return;
-    }
-    const int64_t u0 = U * blockIdx.x / blocks, u1 = U * (blockIdx.x + 1) / blocks;
-    if (before <= u0 && u0 < before + mine) {
-        int b = tid * per;
-        int64_t at = before;
-        for (;; ++b) {
-            const int64_t x = (int64_t)units_of(p, b) * pairs_b;
-            if (u0 < at + x || b + 1 == B) break;
-            at += x;
-        }
-        start_b = b;
-        start_unit = at;
-    }
-    __syncthreads();
     Segment seg;
-    seg.b = start_b;
+    int64_t b_unit;
+    const Deal deal = deal_of(p, blockIdx.x, false, deal_smem, seg.b, b_unit);
+    if (seg.b < 0) return;
+    const int64_t u0 = deal.begin(blockIdx.x), u1 = deal.begin(blockIdx.x + 1);
     key_range(p, seg.b, seg.first, seg.len);
     seg.nu = units_between(seg.first, seg.len);
     seg.u = u0;
-    seg.pr = (int)((u0 - start_unit) / seg.nu);
-    seg.t0 = (int)((u0 - start_unit) % seg.nu);
+    seg.pr = (int)((u0 - b_unit) / seg.nu);
+    seg.t0 = (int)((u0 - b_unit) % seg.nu);
     seg.t1 = (int)min((int64_t)seg.nu, seg.t0 + (u1 - u0));
-    Header header = {-1, 0};
 
     // The tile to load next.  Its page-table entries are read when it becomes that, a whole tile's
     // work before they are needed.
@@ -615,12 +635,6 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nu;
         Part<M::ROWS, D>* part =
             static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * blockIdx.x + (seg.t0 == 0);
-        if (!whole && seg.t0 == 0) {
-            // the block that holds unit x is the largest c with floor(c U / blocks) <= x
-            const int64_t x = seg.u + seg.nu - 1;
-            header.pair = (seg.b * p.pool.H + h) * p.QG + qg;
-            header.parts = (int)(((x + 1) * blocks - 1) / U - blockIdx.x) + 1;
-        }
         float* mine_put =
             reinterpret_cast<float*>(ring + (stage == 0 ? S - 1 : stage - 1) * 2 * HALF);
         if (lane == 0) wput[warp] = mine_put;
@@ -667,68 +681,83 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         }
         seg = nx;
     }
-    if (tid == 0) p.headers[blockIdx.x] = header;
 }
 
 // Block (c, r) joins row r of the parts of the pair that block c of the kernel above began and
-// did not finish: a warp a quarter of the parts, a lane D / 32 dimensions.
+// did not finish: a warp a quarter of the parts, a lane D / 32 dimensions.  Which pair that is
+// follows from the lengths, so this kernel finds it out while the other is still at work.
 template <class M>
-__global__ void __launch_bounds__(JOIN_NT) paged_join_kernel(const Params p) {
+__global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
     using T = typename M::T;
-    constexpr int D = M::D, E = D / 32, JW = JOIN_NT / 32, UN = 4;
+    constexpr int D = M::D, E = D / 32, UN = 8;
+    __shared__ DealSmem deal_smem;
     __shared__ float w[GRID];            // the parts' maxima, then their weights
-    __shared__ float sums[JW][D], red[JW];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y;
-    // sequences without keys: zeros, with nothing to wait for
-    for (int b = blockIdx.x; b < p.table.S; b += GRID)
+    __shared__ float sums[NW][D], red[2][NW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y, c = blockIdx.x;
+    // sequences without keys: zeros
+    for (int b = c; b < p.table.S; b += GRID)
         if (units_of(p, b) == 0)
             for (int i = r; i < p.Hq; i += gridDim.y) {
-                for (int e = tid; e < D; e += JOIN_NT)
+                for (int e = tid; e < D; e += NT)
                     static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * D + e] = from_f32<T>(0.f);
                 if (p.lse && tid == 0) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
             }
+    int b;
+    int64_t b_unit;
+    const Deal deal = deal_of(p, c, true, deal_smem, b, b_unit);
+    int n = 0, row0 = 0, rows = 0;                         // parts; their first query row, rows
+    if (b >= 0) {
+        const int64_t u0 = deal.begin(c), u1 = deal.begin(c + 1);
+        const int nu = units_of(p, b), pr = (int)((u1 - 1 - b_unit) / nu);
+        const int64_t pair0 = b_unit + (int64_t)pr * nu;   // the pair's first unit
+        if (pair0 >= u0 && pair0 + nu > u1) n = deal.block_of(pair0 + nu - 1) - c + 1;
+        row0 = pr / p.QG * p.G + pr % p.QG * M::ROWS;
+        rows = min(M::ROWS, p.G - pr % p.QG * M::ROWS);
+    }
+    // every block waits: the end of this kernel is to mean the end of both
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x;
-    const Header hd = p.headers[c];
-    if (hd.pair < 0) return;
-    const int qg = hd.pair % p.QG;
-    if (r >= min(M::ROWS, p.G - qg * M::ROWS)) return;
-    const int64_t head = (int64_t)(hd.pair / p.QG) * p.G + qg * M::ROWS + r;
+    if (n == 0 || r >= rows) return;
+    const int64_t head = (int64_t)b * p.Hq + row0 + r;
     const Part<M::ROWS, D>* parts = static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c;
     // part k: the tail of block c, then the heads of those that follow
+    float x[UN][E];
+    auto fetch = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            const int k = k0 + i * NW;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[i][e] = k < n ? parts[2 * k + (k == 0)].a[r][lane + 32 * e] : 0.f;
+        }
+    };
+    fetch(warp);                                           // on their way beside the maxima
     float mx = -INFINITY;
-    for (int k = tid; k < hd.parts; k += JOIN_NT) {
+    for (int k = tid; k < n; k += NT) {
         w[k] = parts[2 * k + (k == 0)].m[r];
         mx = fmaxf(mx, w[k]);
     }
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    if (lane == 0) red[warp] = mx;
+    if (lane == 0) red[0][warp] = mx;
     __syncthreads();
-    for (int i = 0; i < JW; ++i) mx = fmaxf(mx, red[i]);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) mx = fmaxf(mx, red[0][i]);
     const float base = mx == -INFINITY ? 0.f : mx;
     float z = 0.f;
-    for (int k = tid; k < hd.parts; k += JOIN_NT) {
+    for (int k = tid; k < n; k += NT) {
         const float f = ex2(w[k] - base);
         w[k] = f;
         z += f * parts[2 * k + (k == 0)].l[r];
     }
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
+    if (lane == 0) red[1][warp] = z;
     __syncthreads();
-    if (lane == 0) red[warp] = z;
     float a[E] = {};
-    for (int k0 = warp; k0 < hd.parts; k0 += JW * UN) {
-        float x[UN][E];
+    for (int k0 = warp; k0 < n; k0 += NW * UN) {
+        if (k0 != warp) fetch(k0);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int k = k0 + i * JW;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[i][e] = k < hd.parts ? parts[2 * k + (k == 0)].a[r][lane + 32 * e] : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < UN; ++i) {
-            const int k = k0 + i * JW;
-            const float f = k < hd.parts ? w[k] : 0.f;
+            const int k = k0 + i * NW;
+            const float f = k < n ? w[k] : 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) a[e] = fmaf(f, x[i][e], a[e]);
         }
@@ -737,11 +766,13 @@ __global__ void __launch_bounds__(JOIN_NT) paged_join_kernel(const Params p) {
     for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = a[e];
     __syncthreads();
     z = 0.f;
-    for (int i = 0; i < JW; ++i) z += red[i];
-    for (int e = tid; e < D; e += JOIN_NT) {
-        float x = 0.f;
-        for (int i = 0; i < JW; ++i) x += sums[i][e];
-        static_cast<T*>(p.o)[head * D + e] = from_f32<T>(x / z);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) z += red[1][i];
+    for (int e = tid; e < D; e += NT) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) y += sums[i][e];
+        static_cast<T*>(p.o)[head * D + e] = from_f32<T>(y / z);
     }
     if (p.lse && tid == 0) p.lse[head] = (mx + log2f(z)) * LN2;
 }
@@ -761,7 +792,7 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(GRID, M::ROWS < p.G ? M::ROWS : p.G);
-    cfg.blockDim = dim3(JOIN_NT);
+    cfg.blockDim = dim3(NT);
     cfg.stream = stream;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
@@ -791,8 +822,7 @@ cudaError_t launch_d(bool bf16, int rows, Params& p, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_attn_workspace(bool bf16, int Hq, int Hkv, int d) {
-    const size_t head = (GRID * sizeof(Header) + 255) / 256 * 256;
-    return head + (size_t)2 * GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
+    return (size_t)2 * GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
@@ -808,8 +838,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.o = a.o;
     p.lse = a.lse;
     p.status = a.status;
-    p.headers = static_cast<Header*>(a.workspace);
-    p.parts = static_cast<unsigned char*>(a.workspace) + (GRID * sizeof(Header) + 255) / 256 * 256;
+    p.parts = a.workspace;
     const int rows = rows_of(a.bf16, p.G);
     return a.d == 64 ? launch_d<64>(a.bf16, rows, p, stream) : launch_d<128>(a.bf16, rows, p, stream);
 }

@@ -4,9 +4,12 @@
 // Which pages are free is ref[p] == 0, nothing else: no free list to keep in step.  A call that
 // takes pages takes the lowest free ones, row after row, so the outcome depends on the inputs
 // alone.  Finding them is a ranking of the free pages (how many free pages lie below p), which a
-// cluster of CL blocks does in one launch: every warp counts a contiguous slice of ref by ballots,
-// the blocks exchange their counts through distributed shared memory, and a second walk over a
-// slice, only by warps that need it, hands out the ranks.
+// cluster of CL blocks does in one launch: ref is cut into up to MAXCH chunks, warps count the
+// free pages of theirs and leave the counts in every block's shared memory (distributed shared
+// memory), each block sums them up, and the chunks that hold pages to hand out are dealt over the
+// cluster's warps once more.  What is to be done to keys, values and tables follows in a second
+// kernel over the whole GPU, launched as a dependent of the first, whose end it waits for on the
+// device.
 #include <limits.h>
 
 #include <cooperative_groups.h>
@@ -23,144 +26,290 @@ namespace {
 constexpr int CL = 8;                  // blocks of a planning cluster (the portable maximum)
 constexpr int PNT = 1024;
 constexpr int PNW = PNT / 32;
+constexpr int MAXCH = 4 * PNT;         // chunks of ref
+constexpr int GROUP = 4;               // chunks a warp counts at once: 16 loads in flight a lane
+constexpr int GRID = 148 * 4;          // blocks of the kernels that carry a plan out
+constexpr int NT = 256;
+constexpr int64_t FORK_ALONE = 1 << 17;   // pairs x table entries that one fork kernel does
 
-// Exclusive sum of x over the block's threads, and the total.  `sums` has PNW entries.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sums, int64_t& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = x;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    return before + incl - x;
-}
-
-// The slice of ref that a warp of the cluster ranks.
-struct Slice {
-    int lo, hi;
+// Exclusive sums of x and y over the block's threads, and the totals.  `sums` has 2 PNW entries.
+struct Sums {
+    int64_t x, all_x;
+    int y, all_y;
 };
 
-__device__ __forceinline__ Slice warp_slice(int n_pages, int rank) {
-    const int64_t warps = CL * PNW, w = rank * PNW + (threadIdx.x >> 5);
-    const int64_t step = ((n_pages + warps - 1) / warps + 31) / 32 * 32;
-    const int64_t lo = w * step, hi = lo + step;
-    return {(int)(lo < n_pages ? lo : n_pages), (int)(hi < n_pages ? hi : n_pages)};
-}
-
-// Free pages of the slice, counted by the whole warp.
-__device__ __forceinline__ int count_free(const int32_t* ref, Slice s) {
-    int n = 0;
-    for (int i = s.lo; i < s.hi; i += 32) {
-        const int at = i + (threadIdx.x & 31);
-        n += __popc(__ballot_sync(0xffffffffu, at < s.hi && ref[at] == 0));
-    }
-    return n;
-}
-
-// Free pages before this warp's slice, and in all of the pool.  Ends with a cluster barrier: all
-// blocks' counts are taken.
-__device__ __forceinline__ void rank_free(int mine, int* warp_free, int* block_free, int& before,
-                                          int& total) {
-    cg::cluster_group cluster = cg::this_cluster();
+__device__ __forceinline__ Sums block_scan(int64_t x, int y, int64_t (*sums)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0) warp_free[warp] = mine;
+    int64_t ix = x;
+    int iy = y;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x2 = __shfl_up_sync(0xffffffffu, ix, o);
+        const int y2 = __shfl_up_sync(0xffffffffu, iy, o);
+        if (lane >= o) {
+            ix += x2;
+            iy += y2;
+        }
+    }
+    if (lane == 31) {
+        sums[warp][0] = ix;
+        sums[warp][1] = iy;
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int w = 0; w < PNW; ++w) n += warp_free[w];
-        *block_free = n;
+    int64_t wx = sums[lane][0];              // PNW = 32: every warp scans the warps' sums
+    int wy = (int)sums[lane][1];
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x2 = __shfl_up_sync(0xffffffffu, wx, o);
+        const int y2 = __shfl_up_sync(0xffffffffu, wy, o);
+        if (lane >= o) {
+            wx += x2;
+            wy += y2;
+        }
     }
+    Sums r;
+    r.all_x = __shfl_sync(0xffffffffu, wx, 31);
+    r.all_y = __shfl_sync(0xffffffffu, wy, 31);
+    const int64_t bx = __shfl_sync(0xffffffffu, wx, warp ? warp - 1 : 0);
+    const int by = __shfl_sync(0xffffffffu, wy, warp ? warp - 1 : 0);
+    r.x = (warp ? bx : 0) + ix - x;
+    r.y = (warp ? by : 0) + iy - y;
+    return r;
+}
+
+// The chunks of ref: chunk c is [c * step, c * step + step), cut off at P.
+struct Chunks {
+    int step, n;
+};
+
+__host__ __device__ __forceinline__ Chunks chunks_of(int P) {
+    const int step = ((P + MAXCH - 1) / MAXCH + 127) / 128 * 128;
+    return {step, (P + step - 1) / step};
+}
+
+// Counts each chunk's free pages into `count` [MAXCH] of every block of the cluster.  Starts with
+// the second half of a cluster barrier (whoever calls has arrived) and ends with a whole one: what
+// the cluster's blocks read of the inputs beforehand, no block changes before that.
+__device__ __forceinline__ void count_free(const int32_t* ref, int P, int* count) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x & 31, warp = cluster.block_rank() * PNW + (threadIdx.x >> 5);
+    const Chunks ch = chunks_of(P);
+    bool begun = false;
+    for (int c0 = warp; c0 < ch.n; c0 += CL * PNW * GROUP) {
+        int n[GROUP] = {};
+        for (int i = lane; i < ch.step; i += 128)
+#pragma unroll
+            for (int g = 0; g < GROUP; ++g)
+#pragma unroll
+                for (int u = 0; u < 128; u += 32) {
+                    const int64_t at = (int64_t)(c0 + g * CL * PNW) * ch.step + i + u;
+                    n[g] += at < P && ref[at] == 0;
+                }
+        if (!begun) cluster.barrier_wait();      // every block runs: its shared memory can be written
+        begun = true;
+#pragma unroll
+        for (int g = 0; g < GROUP; ++g) {
+            const int c = c0 + g * CL * PNW;
+            const int sum = __reduce_add_sync(0xffffffffu, n[g]);
+            if (c < ch.n && lane < CL) cluster.map_shared_rank(count, lane)[c] = sum;
+        }
+    }
+    if (!begun) cluster.barrier_wait();
     cluster.sync();
-    before = total = 0;
-    for (unsigned r = 0; r < CL; ++r) {
-        const int n = *cluster.map_shared_rank(block_free, r);
-        if (r < cluster.block_rank()) before += n;
-        total += n;
+}
+
+// Turns the counts into the free pages before each chunk, and returns all of them; the exclusive
+// sum of x over the block's threads goes along.
+__device__ __forceinline__ int rank_free(int P, int* count, int64_t (*sums)[2], int64_t& x) {
+    constexpr int PER = MAXCH / PNT;
+    const Chunks ch = chunks_of(P);
+    int n[PER], mine = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int c = threadIdx.x * PER + k;
+        n[k] = c < ch.n ? count[c] : 0;
+        mine += n[k];
     }
-    for (int w = 0; w < warp; ++w) before += warp_free[w];
+    const Sums r = block_scan(x, mine, sums);
+    x = r.x;
+    int run = r.y;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        count[threadIdx.x * PER + k] = run;
+        run += n[k];
+    }
+    return r.all_y;
+}
+
+// Division by a number known on the host, for dividends below 2^31: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (floor(m n / 2^32) + n) >> s.
+struct FastDiv {
+    uint32_t d, m;
+    int s;
+
+    explicit FastDiv(uint32_t x) : d(x), s(0) {
+        while ((1u << s) < d) ++s;
+        m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
+
+// A page as 16-byte pieces, in the order of its addresses: heads inside tokens, or tokens inside
+// heads where heads lie further apart.
+struct Pieces {
+    FastDiv outer, row;          // pieces an outer step, pieces a row
+    int64_t so, si;              // bytes an outer step, an inner one
+    int total;                   // pieces a page
+    bool tokens_inside;
+
+    explicit Pieces(const PagedPool& p)
+        : outer((uint32_t)((p.sh > p.st ? 1 << p.page_shift : p.H) * (p.row_bytes / 16))),
+          row((uint32_t)(p.row_bytes / 16)),
+          so(p.sh > p.st ? p.sh : p.st),
+          si(p.sh > p.st ? p.st : p.sh),
+          total((int)(p.H * (p.row_bytes / 16) << p.page_shift)),
+          tokens_inside(p.sh > p.st) {}
+};
+
+constexpr int COPY_U = 4;                    // pieces of keys, and of values, in flight a thread
+constexpr int COPY_CHUNK = NT * COPY_U;      // pieces of one block's step
+
+// The pieces [c0, c0 + COPY_CHUNK) of the slots below `slots` of page `from`, to page `to`.
+__device__ __forceinline__ void copy_chunk(const PagedPool& p, const Pieces& pc, int64_t from,
+                                           int64_t to, int c0, int slots) {
+    uint4 k[COPY_U], v[COPY_U];
+    int64_t off[COPY_U];
+#pragma unroll
+    for (int u = 0; u < COPY_U; ++u) {
+        const uint32_t c = c0 + u * NT + threadIdx.x;
+        const uint32_t o = pc.outer.div(c), r = c - o * pc.outer.d, i = pc.row.div(r);
+        off[u] = -1;
+        if (c < (uint32_t)pc.total && (int)(pc.tokens_inside ? i : o) < slots) {
+            off[u] = o * pc.so + i * pc.si + (r - i * pc.row.d) * 16;
+            k[u] = *reinterpret_cast<const uint4*>(p.k + from * p.sp + off[u]);
+            v[u] = *reinterpret_cast<const uint4*>(p.v + from * p.sp + off[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < COPY_U; ++u)
+        if (off[u] >= 0) {
+            *reinterpret_cast<uint4*>(p.k + to * p.sp + off[u]) = k[u];
+            *reinterpret_cast<uint4*>(p.v + to * p.sp + off[u]) = v[u];
+        }
+}
+
+// Up to 24 KB beside a kernel's own arrays need no leave.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    if (bytes <= 24 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// Launch a kernel that may start before the one launched last has ended; it waits for that end
+// itself (wait_for_plan).
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), int blocks, int threads, size_t smem,
+                             cudaStream_t stream, const Args&... args) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+__device__ __forceinline__ void let_dependents_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void wait_for_plan() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------------
-// append: a copy of every token's row of heads to its slot.
+// append: a copy of every token's row of heads to its slot.  Bound by HBM, each byte read and
+// written once; with few tokens by the chain row -> position -> page -> copy, so a warp's lanes
+// find the places of its tokens side by side, and a warp takes several only when there are more
+// tokens than warps to go round.
 
-constexpr int AP_NT = 256;
-constexpr int AP_TOK = 8;              // tokens a warp takes one after another
+constexpr int AP_MAXTOK = 8;           // tokens of one warp
+constexpr int AP_U = 4;                // pieces of keys, and of values, in flight a lane
 
-__global__ void __launch_bounds__(AP_NT) append_kernel(const PagedAppendArgs a) {
+// The last of S rows that begins at or before token i (the first, if none does).
+__device__ __forceinline__ int row_of(const int32_t* cu, int S, int64_t i) {
     const int lane = threadIdx.x & 31;
-    const int64_t i0 = ((int64_t)blockIdx.x * (AP_NT / 32) + (threadIdx.x >> 5)) * AP_TOK;
-    const int64_t cap = (int64_t)a.table.max_pages << a.pool.page_shift;
-    const int cpr = a.pool.row_bytes / 16;       // 16-byte pieces of a row
-    int b = 0;
-    if (a.cu_seqlens) {                           // the last row that begins at or before i0
-        int hi = a.table.S - 1;
-        while (b < hi) {
-            const int mid = (b + hi + 1) >> 1;
-            if (a.cu_seqlens[mid] <= i0) b = mid;
-            else hi = mid - 1;
-        }
+    int lo = 0, n = S;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const bool below = lane * step < n && (lane == 0 || cu[lo + lane * step] <= i);
+        const int last = __popc(__ballot_sync(0xffffffffu, below)) - 1;
+        lo += last * step;
+        n = min(step, n - last * step);
     }
-    for (int64_t i = i0; i < i0 + AP_TOK && i < a.T; ++i) {
-        int64_t at;
+    return lo;
+}
+
+__global__ void __launch_bounds__(NT) append_kernel(const PagedAppendArgs a, const FastDiv token,
+                                                    const FastDiv row, const int tok) {
+    const int lane = threadIdx.x & 31;
+    const int64_t i0 = ((int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5)) * tok;
+    if (i0 >= a.T) return;
+    const int64_t i = i0 + lane;                  // this lane's token
+    int64_t slot = -1;
+    int b = a.cu_seqlens ? row_of(a.cu_seqlens, a.table.S, i0) : (int)i;
+    if (lane < tok && i < a.T) {
+        int64_t at = 0;
+        bool in = true;
         if (a.cu_seqlens) {
             while (b < a.table.S && a.cu_seqlens[b + 1] <= i) ++b;
-            if (b == a.table.S) return;           // behind the last sequence
-            if (i < a.cu_seqlens[b]) continue;    // before the first one
-            at = i - a.cu_seqlens[b];
-        } else {
-            b = (int)i;
-            at = 0;
+            in = b < a.table.S && i >= a.cu_seqlens[b];     // not around the sequences
+            if (in) at = i - a.cu_seqlens[b];
         }
-        const int pos = a.pos[b];
-        if (pos < 0) continue;
-        at += pos;
-        if (at >= cap) {
-            if (lane == 0) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
-            continue;
-        }
-        const int id = a.table.entries[b * a.table.stride + (at >> a.pool.page_shift)];
-        if ((unsigned)id >= (unsigned)a.pool.n_pages) {
-            if (lane == 0) paged_flag(a.status, GRET_PAGED_BAD_PAGE);
-            continue;
-        }
-        const int64_t slot = id * a.pool.sp + (at & ((1 << a.pool.page_shift) - 1)) * a.pool.st;
-        for (int c = lane; c < a.pool.H * cpr; c += 32) {
-            const int h = c / cpr, x = (c % cpr) * 16;
-            const uint4 kx = *reinterpret_cast<const uint4*>(a.k + i * a.kt + h * a.kh + x);
-            const uint4 vx = *reinterpret_cast<const uint4*>(a.v + i * a.vt + h * a.vh + x);
-            *reinterpret_cast<uint4*>(a.pool.k + slot + h * a.pool.sh + x) = kx;
-            *reinterpret_cast<uint4*>(a.pool.v + slot + h * a.pool.sh + x) = vx;
+        const int pos = in ? a.pos[b] : -1;
+        if (pos >= 0) {
+            at += pos;
+            if (at >= (int64_t)a.table.max_pages << a.pool.page_shift) {
+                paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
+            } else {
+                const int id = a.table.entries[b * a.table.stride + (at >> a.pool.page_shift)];
+                if ((unsigned)id >= (unsigned)a.pool.n_pages)
+                    paged_flag(a.status, GRET_PAGED_BAD_PAGE);
+                else
+                    slot = id * a.pool.sp + (at & ((1 << a.pool.page_shift) - 1)) * a.pool.st;
+            }
         }
     }
-}
-
-// Slots [0, slots) of page `from` to page `to`, by the whole block.
-__device__ __forceinline__ void copy_slots(const PagedPool& p, int64_t from, int64_t to, int slots) {
-    const int cpr = p.row_bytes / 16, per = p.H * cpr;
-    for (int c = threadIdx.x; c < slots * per; c += blockDim.x) {
-        const int t = c / per, h = c % per / cpr;
-        const int64_t off = t * p.st + h * p.sh + (c % cpr) * 16;
-        const uint4 kx = *reinterpret_cast<const uint4*>(p.k + from * p.sp + off);
-        const uint4 vx = *reinterpret_cast<const uint4*>(p.v + from * p.sp + off);
-        *reinterpret_cast<uint4*>(p.k + to * p.sp + off) = kx;
-        *reinterpret_cast<uint4*>(p.v + to * p.sp + off) = vx;
+    const uint32_t total = min((int64_t)tok, a.T - i0) * token.d;
+    for (uint32_t c0 = 0; c0 < total; c0 += 32 * AP_U) {
+        uint4 k[AP_U], v[AP_U];
+        int64_t to[AP_U];
+#pragma unroll
+        for (int u = 0; u < AP_U; ++u) {
+            const uint32_t c = c0 + u * 32 + lane;
+            const uint32_t t = token.div(c), r = c - t * token.d, h = row.div(r);
+            const uint32_t x = (r - h * row.d) * 16;
+            to[u] = __shfl_sync(0xffffffffu, slot, t & 31);
+            if (c >= total) to[u] = -1;
+            if (to[u] >= 0) {
+                to[u] += h * a.pool.sh + x;
+                k[u] = *reinterpret_cast<const uint4*>(a.k + (i0 + t) * a.kt + h * a.kh + x);
+                v[u] = *reinterpret_cast<const uint4*>(a.v + (i0 + t) * a.vt + h * a.vh + x);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < AP_U; ++u)
+            if (to[u] >= 0) {
+                *reinterpret_cast<uint4*>(a.pool.k + to[u]) = k[u];
+                *reinterpret_cast<uint4*>(a.pool.v + to[u]) = v[u];
+            }
     }
 }
 
 // ---------------------------------------------------------------------------------------------
-// resize: a plan by one cluster (who gets which page), then one block a row carries it out.
-
-// What the plan says of a row that grows; else it holds the page to copy from.
-enum : int { PLAN_NO_COPY = -1, PLAN_REFUSED = -2 };
+// resize: a plan by one cluster (who gets which page), then the whole GPU carries it out.
 
 // A row's change, from its length before the call.
 struct Change {
@@ -177,14 +326,18 @@ __device__ __forceinline__ Change change_of(const PagedResizeArgs& a, int s) {
     return c;
 }
 
+// Leaves pos, the new pages' ref and table entries, and in workspace[s] the page that row s is to
+// copy its last, partly filled one from (-1: none).
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     resize_plan_kernel(const PagedResizeArgs a) {
     extern __shared__ int rows_smem[];
-    __shared__ int64_t sums[PNW];
-    __shared__ int warp_free[PNW], block_free;
+    __shared__ int64_t sums[PNW][2];
+    __shared__ int chunk_before[MAXCH];
     int* upto = rows_smem;                        // [S] pages asked for by rows 0 .. s
     int* first = rows_smem + a.table.S;           // [S] table entry the first of them goes to
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();
+    let_dependents_start();
     const int tid = threadIdx.x, lane = tid & 31, S = a.table.S;
     const bool lead = cluster.block_rank() == 0;
     const int shift = a.pool.page_shift;
@@ -195,15 +348,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     int64_t mine = 0;
     for (int s = s0; s < s1; ++s) {
         const Change c = change_of(a, s);
-        int need = 0, src = PLAN_NO_COPY;
+        int need = 0, src = -1;
+        bool grown = false;
         first[s] = 0;
         if (c.bad) {
             if (lead) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
-            src = PLAN_REFUSED;
         } else if (c.n1 > c.n0) {
             if (c.n1 > (int64_t)a.table.max_pages << shift) {
                 if (lead) paged_flag(a.status, GRET_PAGED_TABLE_FULL);
-                src = PLAN_REFUSED;
             } else {
                 const int c0 = pages_of(c.n0, shift), c1 = pages_of(c.n1, shift);
                 if (c.n0 & ((1 << shift) - 1)) {
@@ -216,21 +368,24 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
                 }
                 need = c1 - c0 + (src >= 0);
                 first[s] = c0 - (src >= 0);
+                grown = true;
             }
         }
         upto[s] = need;
-        if (lead) a.workspace[s] = src;
+        if (lead) {
+            a.workspace[s] = src;
+            a.pos[s] = grown ? (int)c.n0 : -1;
+        }
         mine += need;
     }
-    int64_t asked;
-    int64_t run = block_scan(mine, sums, asked);
+    count_free(a.ref, a.pool.n_pages, chunk_before);
+    int64_t run = mine;
+    const int total = rank_free(a.pool.n_pages, chunk_before, sums, run);
     for (int s = s0; s < s1; ++s) {
         run += upto[s];
         upto[s] = (int)(run < INT_MAX ? run : INT_MAX);
     }
-    const Slice slice = warp_slice(a.pool.n_pages, cluster.block_rank());
-    int before, total;
-    rank_free(count_free(a.ref, slice), warp_free, &block_free, before, total);
+    __syncthreads();
     // rows up to `last` that ask for pages get them: upto rises, so the others follow
     int lo = 0, hi = S;
     while (lo < hi) {
@@ -240,103 +395,227 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     }
     const int granted = lo ? upto[lo - 1] : 0;
     if (lead)
-        for (int s = lo + tid; s < S; s += PNT) {
+        for (int s = max(lo, s0); s < s1; ++s) {   // the thread that wrote the row's plan
             const Change c = change_of(a, s);
-            const int src = a.workspace[s];
-            if (c.n1 > c.n0 && src != PLAN_REFUSED &&
-                (src >= 0 || pages_of(c.n1, shift) > pages_of(c.n0, shift))) {
-                a.workspace[s] = PLAN_REFUSED;
+            if (a.pos[s] >= 0 &&
+                (a.workspace[s] >= 0 || pages_of(c.n1, shift) > pages_of(c.n0, shift))) {
+                a.pos[s] = a.workspace[s] = -1;
                 paged_flag(a.status, GRET_PAGED_NO_PAGES);
             }
         }
     // hand out the free pages of rank < granted
-    for (int i = slice.lo; i < slice.hi && before < granted; i += 32) {
-        const int at = i + lane;
-        const bool free = at < slice.hi && a.ref[at] == 0;
-        const unsigned mask = __ballot_sync(0xffffffffu, free);
-        const int rank = before + __popc(mask & ((1u << lane) - 1));
-        if (free && rank < granted) {
-            int l = 0, r = S - 1;                 // the first row with upto > rank
-            while (l < r) {
-                const int mid = (l + r) >> 1;
-                if (upto[mid] > rank) r = mid;
-                else l = mid + 1;
+    const Chunks ch = chunks_of(a.pool.n_pages);
+    const int warp = cluster.block_rank() * PNW + (tid >> 5);
+    for (int c = warp; c < ch.n && chunk_before[c] < granted; c += CL * PNW) {
+        int before = chunk_before[c];
+        const int64_t begin = (int64_t)c * ch.step;
+        for (int i = 0; i < ch.step && before < granted; i += 128) {
+            bool free[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t at = begin + i + 32 * u + lane;
+                free[u] = at < a.pool.n_pages && a.ref[at] == 0;
             }
-            a.table.entries[l * a.table.stride + first[l] + rank - (l ? upto[l - 1] : 0)] = at;
-            a.ref[at] = 1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at = (int)(begin + i + 32 * u + lane);
+                const unsigned mask = __ballot_sync(0xffffffffu, free[u]);
+                const int rank = before + __popc(mask & ((1u << lane) - 1));
+                if (free[u] && rank < granted) {
+                    int l = 0, r = S - 1;         // the first row with upto > rank
+                    while (l < r) {
+                        const int mid = (l + r) >> 1;
+                        if (upto[mid] > rank) r = mid;
+                        else l = mid + 1;
+                    }
+                    a.table.entries[l * a.table.stride + first[l] + rank - (l ? upto[l - 1] : 0)] =
+                        at;
+                    a.ref[at] = 1;
+                }
+                before += __popc(mask);
+            }
         }
-        before += __popc(mask);
     }
-    cluster.sync();   // no block leaves while another reads its count
 }
 
-__global__ void __launch_bounds__(256) resize_apply_kernel(const PagedResizeArgs a) {
-    const int s = blockIdx.x, shift = a.pool.page_shift;
-    const Change c = change_of(a, s);
-    const int plan = a.workspace[s];
-    int32_t* row = a.table.entries + s * a.table.stride;
-    const int c0 = pages_of(c.n0, shift);
-    bool done = false;
-    if (!c.bad && c.n1 > c.n0 && plan != PLAN_REFUSED) {
-        done = true;
-        if (plan >= 0) {
-            copy_slots(a.pool, plan, row[c0 - 1], (int)(c.n0 & ((1 << shift) - 1)));
-            if (threadIdx.x == 0 && atomicSub(&a.ref[plan], 1) <= 0) {
-                atomicAdd(&a.ref[plan], 1);
-                paged_flag(a.status, GRET_PAGED_BAD_COUNT);
-            }
+__device__ __forceinline__ void drop_page(const PagedResizeArgs& a, int id) {
+    if (atomicSub(&a.ref[id], 1) <= 0) {
+        atomicAdd(&a.ref[id], 1);
+        paged_flag(a.status, GRET_PAGED_BAD_COUNT);
+    }
+}
+
+// The entries [j0, j1) of a row, by the whole block: four a thread on their way at a time.
+__device__ __forceinline__ void drop_entries(const PagedResizeArgs& a, int32_t* row, int j0, int j1) {
+    constexpr int U = 4;
+    for (int j = j0 + threadIdx.x; j < j1; j += NT * U) {
+        int id[U], had[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = j + u * NT < j1 ? row[j + u * NT] : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            had[u] = 1;
+            if ((unsigned)id[u] < (unsigned)a.pool.n_pages) had[u] = atomicSub(&a.ref[id[u]], 1);
         }
-    } else if (!c.bad && c.n1 < c.n0) {
-        for (int j = pages_of(c.n1, shift) + threadIdx.x; j < c0; j += blockDim.x) {
-            const int id = row[j];
-            row[j] = -1;
-            if ((unsigned)id >= (unsigned)a.pool.n_pages) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j + u * NT >= j1) continue;
+            row[j + u * NT] = -1;
+            if ((unsigned)id[u] >= (unsigned)a.pool.n_pages) {
                 paged_flag(a.status, GRET_PAGED_BAD_PAGE);
-            } else if (atomicSub(&a.ref[id], 1) <= 0) {
-                atomicAdd(&a.ref[id], 1);
+            } else if (had[u] <= 0) {
+                atomicAdd(&a.ref[id[u]], 1);
                 paged_flag(a.status, GRET_PAGED_BAD_COUNT);
             }
         }
     }
-    __syncthreads();   // every thread has read the length
-    if (threadIdx.x == 0) {
-        a.pos[s] = done ? (int)c.n0 : -1;
-        if (done || (!c.bad && c.n1 < c.n0)) a.seq_lens[s] = (int)c.n1;
+}
+
+__global__ void __launch_bounds__(NT) resize_apply_kernel(const PagedResizeArgs a,
+                                                          const Pieces pc) {
+    __shared__ int from[NT], to[NT], slots[NT], copies;
+    const int tid = threadIdx.x, S = a.table.S, shift = a.pool.page_shift;
+    wait_for_plan();
+    // a block a row: pages that it drops, its new length
+    for (int s = blockIdx.x; s < S; s += GRID) {
+        const Change c = change_of(a, s);
+        const bool grown = a.pos[s] >= 0, shrunk = !c.bad && c.n1 < c.n0;
+        if (shrunk) {
+            drop_entries(a, a.table.entries + s * a.table.stride, pages_of(c.n1, shift),
+                         pages_of(c.n0, shift));
+        } else if (grown && tid == 0 && a.workspace[s] >= 0) {
+            drop_page(a, a.workspace[s]);
+        }
+        __syncthreads();   // every thread has read the length
+        if (tid == 0 && (grown || shrunk)) a.seq_lens[s] = (int)c.n1;
+    }
+    // the copies, NT rows at a time, in steps dealt over all blocks.  pos is the old length
+    const int steps = (pc.total + COPY_CHUNK - 1) / COPY_CHUNK;
+    int next = blockIdx.x;                        // this block's next step, counted from the batch's first
+    for (int s0 = 0; s0 < S; s0 += NT) {
+        __syncthreads();
+        if (tid == 0) copies = 0;
+        __syncthreads();
+        const int s = s0 + tid;
+        if (s < S && a.workspace[s] >= 0) {
+            const int n0 = a.pos[s], k = atomicAdd(&copies, 1);
+            from[k] = a.workspace[s];
+            to[k] = a.table.entries[s * a.table.stride + (n0 >> shift)];
+            slots[k] = n0 & ((1 << shift) - 1);
+        }
+        __syncthreads();
+        const int64_t all = (int64_t)copies * steps;
+        int64_t i = next;
+        for (; i < all; i += GRID) {
+            const int k = (int)(i / steps), c0 = (int)(i % steps) * COPY_CHUNK;
+            if (pc.tokens_inside || c0 < slots[k] * (int)pc.outer.d)
+                copy_chunk(a.pool, pc, from[k], to[k], c0, slots[k]);
+        }
+        next = (int)(i - all);
     }
 }
 
 // ---------------------------------------------------------------------------------------------
-// fork: one block a pair.
+// fork.  The copy of the table entries is bound by HBM (L2, for the rows that many share).  The
+// counts are bound by atomics on one address where many pairs share a source and each adds its 1:
+// there, of the m pairs of a source each adds m to an m-th of its pages.  That takes the pairs'
+// knowing of one another, so that the lengths, by which a pair that has no effect is known, can
+// only be set by a second kernel; small calls go without.
 
-__global__ void __launch_bounds__(256) fork_kernel(const PagedForkArgs a) {
-    const int i = blockIdx.x, S = a.table.S;
-    const int s = a.src[i], d = a.dst[i];
-    bool bad = (unsigned)s >= (unsigned)S || (unsigned)d >= (unsigned)S || s == d;
-    // refused: a destination that an earlier pair names, a source that is a destination
-    for (int j = threadIdx.x; j < a.n; j += blockDim.x) {
-        const int x = a.dst[j];
-        bad |= (j < i && x == d) || x == s;
+// The first pair that names each row as its destination (INT_MAX: none).
+__device__ __forceinline__ void first_pairs(const PagedForkArgs& a, int* first) {
+    for (int s = threadIdx.x; s < a.table.S; s += NT) first[s] = INT_MAX;
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.n; j += NT) {
+        const int d = a.dst[j];
+        if ((unsigned)d < (unsigned)a.table.S) atomicMin(&first[d], j);
     }
-    int64_t n = 0;
-    if (!__syncthreads_or(bad)) {
-        n = a.seq_lens[s];
-        bad = a.seq_lens[d] != 0 || n < 0 || n > (int64_t)a.table.max_pages << a.page_shift;
-    } else {
-        bad = true;
+    __syncthreads();
+}
+
+// Whether pair j takes effect.  seq_lens as before the call.
+__device__ __forceinline__ bool takes_effect(const PagedForkArgs& a, const int* first, int j) {
+    const int s = a.src[j], d = a.dst[j], S = a.table.S;
+    if ((unsigned)s >= (unsigned)S || (unsigned)d >= (unsigned)S) return false;
+    const int n = a.seq_lens[s];
+    return first[d] == j && first[s] == INT_MAX && a.seq_lens[d] == 0 && n >= 0 &&
+           n <= (int64_t)a.table.max_pages << a.page_shift;
+}
+
+template <bool SHARE>
+__global__ void __launch_bounds__(NT) fork_kernel(const PagedForkArgs a) {
+    extern __shared__ int first[];
+    __shared__ int before[NT / 32], siblings[NT / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (SHARE) let_dependents_start();
+    first_pairs(a, first);
+    for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+        if (!takes_effect(a, first, i)) {
+            if (blockIdx.y == 0 && tid == 0) paged_flag(a.status, GRET_PAGED_BAD_ROW);
+            continue;
+        }
+        const int s = a.src[i], d = a.dst[i], n = a.seq_lens[s];
+        const int held = pages_of(n, a.page_shift);
+        int lo = 0, hi = held, add = 1;           // the entries whose pages it counts
+        if (SHARE) {
+            int k = 0, m = 0;                     // pairs of this source before i, and in all
+            for (int j = tid; j < a.n; j += NT)
+                if (a.src[j] == s && takes_effect(a, first, j)) {
+                    ++m;
+                    k += j < i;
+                }
+            k = __reduce_add_sync(0xffffffffu, k);
+            m = __reduce_add_sync(0xffffffffu, m);
+            __syncthreads();
+            if (lane == 0) {
+                before[warp] = k;
+                siblings[warp] = m;
+            }
+            __syncthreads();
+            k = m = 0;
+            for (int w = 0; w < NT / 32; ++w) {
+                k += before[w];
+                m += siblings[w];
+            }
+            lo = (int)((int64_t)held * k / m);
+            hi = (int)((int64_t)held * (k + 1) / m);
+            add = m;
+        }
+        const int32_t* from = a.table.entries + s * a.table.stride;
+        int32_t* to = a.table.entries + d * a.table.stride;
+        constexpr int U = 4;
+        for (int j0 = blockIdx.y * NT * U; j0 < held; j0 += gridDim.y * NT * U) {
+            int id[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u * NT + tid;
+                if (j < held) id[u] = from[j];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = j0 + u * NT + tid;
+                if (j >= held) continue;
+                to[j] = id[u];
+                if (j < lo || j >= hi) continue;
+                if ((unsigned)id[u] < (unsigned)a.n_pages) atomicAdd(&a.ref[id[u]], add);
+                else paged_flag(a.status, GRET_PAGED_BAD_PAGE);
+            }
+        }
+        if (!SHARE) {
+            __syncthreads();                      // every thread has read the lengths
+            if (tid == 0) a.seq_lens[d] = n;
+        }
     }
-    __syncthreads();   // every thread has read the lengths
-    if (bad) {
-        if (threadIdx.x == 0) paged_flag(a.status, GRET_PAGED_BAD_ROW);
-        return;
-    }
-    const int held = pages_of(n, a.page_shift);
-    for (int j = threadIdx.x; j < held; j += blockDim.x) {
-        const int id = a.table.entries[s * a.table.stride + j];
-        a.table.entries[d * a.table.stride + j] = id;
-        if ((unsigned)id < (unsigned)a.n_pages) atomicAdd(&a.ref[id], 1);
-        else paged_flag(a.status, GRET_PAGED_BAD_PAGE);
-    }
-    if (threadIdx.x == 0) a.seq_lens[d] = (int)n;
+}
+
+// The destinations' lengths, once nobody asks any more whether they are empty.
+__global__ void __launch_bounds__(NT) fork_lengths_kernel(const PagedForkArgs a) {
+    extern __shared__ int first[];
+    first_pairs(a, first);
+    const int i = blockIdx.x * NT + threadIdx.x;
+    const bool ok = i < a.n && takes_effect(a, first, i);
+    wait_for_plan();
+    if (ok) a.seq_lens[a.dst[i]] = a.seq_lens[a.src[i]];
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -355,58 +634,78 @@ __host__ __device__ __forceinline__ CompactPlan compact_plan(const PagedCompactA
 
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     compact_plan_kernel(const PagedCompactArgs a) {
-    __shared__ int warp_free[PNW], block_free;
+    __shared__ int64_t sums[PNW][2];
+    __shared__ int chunk_before[MAXCH];
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();
+    let_dependents_start();
     const int lane = threadIdx.x & 31, P = a.pool.n_pages;
     const CompactPlan plan = compact_plan(a);
-    const Slice slice = warp_slice(P, cluster.block_rank());
-    int holes, total;                              // free pages before the one at hand
-    rank_free(count_free(a.ref, slice), warp_free, &block_free, holes, total);
-    const int L = P - total;
+    count_free(a.ref, P, chunk_before);
+    int64_t none = 0;
+    const int L = P - rank_free(P, chunk_before, sums, none);
+    __syncthreads();
     if (cluster.block_rank() == 0 && threadIdx.x == 0) {
         *a.n_live = L;
         plan.counts[0] = L;
         if (L == P) plan.counts[1] = 0;            // no page has the index L
     }
-    for (int i = slice.lo; i < slice.hi; i += 32) {
-        const int at = i + lane;
-        const bool free = at < slice.hi && a.ref[at] == 0;
-        const unsigned mask = __ballot_sync(0xffffffffu, free);
-        const int h = holes + __popc(mask & ((1u << lane) - 1));
-        if (at < slice.hi) {
-            if (at == L) plan.counts[1] = h;       // holes below L = pages in use past it
-            if (at < L) {
-                if (free) plan.holes[h] = at;
-            } else {
-                plan.rank[at] = free ? -1 : at - h;
-                if (!free) plan.used[at - h] = at;
+    const Chunks ch = chunks_of(P);
+    for (int c = cluster.block_rank() * PNW + (threadIdx.x >> 5); c < ch.n; c += CL * PNW) {
+        int holes = chunk_before[c];               // free pages before the one at hand
+        const int64_t begin = (int64_t)c * ch.step;
+        for (int i = 0; i < ch.step; i += 128) {
+            bool free[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t at = begin + i + 32 * u + lane;
+                free[u] = at < P && a.ref[at] == 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t at = begin + i + 32 * u + lane;
+                const unsigned mask = __ballot_sync(0xffffffffu, free[u]);
+                const int h = holes + __popc(mask & ((1u << lane) - 1));
+                if (at < P) {
+                    if (at == L) plan.counts[1] = h;   // holes below L = pages in use past it
+                    if (at < L) {
+                        if (free[u]) plan.holes[h] = (int)at;
+                    } else {
+                        plan.rank[at] = free[u] ? -1 : (int)at - h;
+                        if (!free[u]) plan.used[at - h] = (int)at;
+                    }
+                }
+                holes += __popc(mask);
             }
         }
-        holes += __popc(mask);
     }
-    cluster.sync();   // no block leaves while another reads its count
 }
 
-__global__ void __launch_bounds__(256) compact_move_kernel(const PagedCompactArgs a) {
+__global__ void __launch_bounds__(NT) compact_move_kernel(const PagedCompactArgs a,
+                                                          const Pieces pc) {
     const CompactPlan plan = compact_plan(a);
+    wait_for_plan();
     const int L = plan.counts[0], moves = plan.counts[1];
-    for (int k = blockIdx.x; k < moves; k += gridDim.x) {
+    const int steps = (pc.total + COPY_CHUNK - 1) / COPY_CHUNK;
+    for (int64_t i = blockIdx.x; i < (int64_t)moves * steps; i += GRID) {
+        const int k = (int)(i / steps), c = (int)(i % steps);
         const int from = plan.used[L - moves + k], to = plan.holes[k];
-        copy_slots(a.pool, from, to, 1 << a.pool.page_shift);
-        if (threadIdx.x == 0) {
+        copy_chunk(a.pool, pc, from, to, c * COPY_CHUNK, 1 << a.pool.page_shift);
+        if (c == 0 && threadIdx.x == 0) {
             a.ref[to] = a.ref[from];
             a.ref[from] = 0;
         }
     }
     const int64_t cap = (int64_t)a.table.max_pages << a.pool.page_shift;
-    for (int s = blockIdx.x; s < a.table.S; s += gridDim.x) {
+    for (int s = blockIdx.x; s < a.table.S; s += GRID) {
         const int64_t n = a.seq_lens[s];
         if (n < 0 || n > cap) {
             if (threadIdx.x == 0) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
             continue;
         }
         int32_t* row = a.table.entries + s * a.table.stride;
-        for (int j = threadIdx.x; j < pages_of(n, a.pool.page_shift); j += blockDim.x) {
+#pragma unroll 4
+        for (int j = threadIdx.x; j < pages_of(n, a.pool.page_shift); j += NT) {
             const int id = row[j];
             if ((unsigned)id >= (unsigned)a.pool.n_pages) {
                 paged_flag(a.status, GRET_PAGED_BAD_PAGE);
@@ -422,35 +721,55 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const PagedCompactArg
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
-    const int64_t per = (int64_t)(AP_NT / 32) * AP_TOK;
-    append_kernel<<<(unsigned)((a.T + per - 1) / per), AP_NT, 0, stream>>>(a);
+    // one token a warp up to a full GPU of warps (148 x 64), then more of them
+    const int64_t even = a.T / (148 * 64);
+    const int tok = (int)(even < 1 ? 1 : even > AP_MAXTOK ? AP_MAXTOK : even);
+    const int64_t per = (int64_t)(NT / 32) * tok;
+    const uint32_t row = a.pool.row_bytes / 16;
+    append_kernel<<<(unsigned)((a.T + per - 1) / per), NT, 0, stream>>>(
+        a, FastDiv(a.pool.H * row), FastDiv(row), tok);
     return cudaGetLastError();
 }
 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)a.table.S * 2 * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(resize_plan_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         PAGED_MAX_SEQS * 2 * (int)sizeof(int));
+    cudaError_t e = allow_smem(resize_plan_kernel, smem);
     if (e != cudaSuccess) return e;
     resize_plan_kernel<<<CL, PNT, smem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    resize_apply_kernel<<<(unsigned)a.table.S, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(resize_apply_kernel, GRID, NT, 0, stream, a, Pieces(a.pool));
 }
 
 cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
-    fork_kernel<<<(unsigned)a.n, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    const size_t smem = (size_t)a.table.S * sizeof(int);
+    const int x = a.n < 2 * GRID ? a.n : 2 * GRID;
+    cudaError_t e;
+    // Alone a block a pair, rows of up to 4 steps of a block, and no more atomics than take a
+    // microsecond or two on few addresses.
+    if (a.table.max_pages <= 4096 && (int64_t)a.n * a.table.max_pages <= FORK_ALONE) {
+        e = allow_smem(fork_kernel<false>, smem);
+        if (e != cudaSuccess) return e;
+        fork_kernel<false><<<x, NT, smem, stream>>>(a);
+        return cudaGetLastError();
+    }
+    e = allow_smem(fork_kernel<true>, smem);
+    if (e == cudaSuccess) e = allow_smem(fork_lengths_kernel, smem);
+    if (e != cudaSuccess) return e;
+    // a block a pair; with few pairs a row is cut up, in pieces of 1024 entries at least
+    int y = 2 * GRID / x, most = (a.table.max_pages + 1023) / 1024;
+    if (y > most) y = most;
+    fork_kernel<true><<<dim3(x, y), NT, smem, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_dependent(fork_lengths_kernel, (a.n + NT - 1) / NT, NT, smem, stream, a);
 }
 
 cudaError_t launch_paged_compact(const PagedCompactArgs& a, cudaStream_t stream) {
     compact_plan_kernel<<<CL, PNT, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    compact_move_kernel<<<148 * 4, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(compact_move_kernel, GRID, NT, 0, stream, a, Pieces(a.pool));
 }
 
 }  // namespace gret
