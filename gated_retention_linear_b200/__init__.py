@@ -4,10 +4,10 @@ A thin Python binding over the C ABI in include/gret.h (libgret.so, built in-tre
 `python gated_retention_linear_b200/build.py`).  The functions here only marshal arguments:
 they read shapes and strides off torch tensors, allocate outputs and workspaces with torch, pass
 raw device pointers and the current CUDA stream, and raise on a non-OK status.  Every step of
-the computation runs in the library's CUDA kernels; there is no fallback.  If libgret.so is
+the computation runs in the library's CUDA kernels; there is no fallback.  The paged cache's
+calls do the same in C++ (csrc/paged_binding.cpp, _paged.so).  If libgret.so or _paged.so is
 missing this import fails.
 """
-import contextlib
 import ctypes
 import os
 
@@ -16,11 +16,14 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgret.so")
 
-if not os.path.exists(LIB_PATH):
-    raise ImportError("libgret.so not found at %s; build it with "
-                      "`python gated_retention_linear_b200/build.py`" % LIB_PATH)
+for _path in (LIB_PATH, os.path.join(_HERE, "_paged.so")):
+    if not os.path.exists(_path):
+        raise ImportError("%s not found at %s; build it with `python gated_retention_linear_b200/"
+                          "build.py`" % (os.path.basename(_path), _path))
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _paged  # noqa: E402  (needs torch and libgret.so loaded)
 
 GRET_F32, GRET_BF16 = 0, 1
 STATUS = {0: "GRET_OK", 1: "GRET_ERR_INVALID_ARG", 2: "GRET_ERR_UNSUPPORTED",
@@ -112,6 +115,9 @@ class GretError(RuntimeError):
 def _check(fn, code):
     if code != 0:
         raise GretError(fn, code)
+
+
+_paged.set_check(_check)
 
 
 def _ptr(t):
@@ -432,64 +438,6 @@ def gret_layer_forward(x, w_qkvg, w_g, H, d=128, cu_seqlens=None, state_in=None,
 GRET_PAGED_BAD_PAGE, GRET_PAGED_BAD_LENGTH, GRET_PAGED_NO_PAGES = 1, 2, 4
 GRET_PAGED_TABLE_FULL, GRET_PAGED_BAD_ROW, GRET_PAGED_BAD_COUNT = 8, 16, 32
 
-_HERE_SCOPE = contextlib.nullcontext()
-
-
-def _paged_scope(device, stream, tensors):
-    """Checks that every tensor is on `device`, a GPU, and returns the context in which a paged
-    call allocates and launches: that device, and `stream` where one is given."""
-    if device.type != "cuda":
-        raise ValueError("paged cache tensors must be on a GPU")
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("paged cache tensors must be on one device")
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError("stream must be of the tensors' device")
-        return torch.cuda.stream(stream)
-    return _HERE_SCOPE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _int32(t, name, *shape):
-    """An int32 argument's data pointer (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be contiguous int32 %s" % (name, list(shape)))
-    return t.data_ptr()
-
-
-def _paged_table(page_table, rows):
-    """(pointer, row stride, entries a row)."""
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != rows
-            or (page_table.shape[1] > 1 and rows and page_table.stride(1) != 1)):
-        raise ValueError("page_table must be int32 [%d, max_pages] with contiguous rows" % rows)
-    max_pages = page_table.shape[1]
-    stride = page_table.stride(0) if rows > 1 else max_pages
-    return page_table.data_ptr(), stride, max_pages
-
-
-def _paged_pool(k_pages, v_pages, head_major):
-    """(k, v, page stride, token stride, head stride, pages, page size, dtype) and (heads, d)."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
-        raise ValueError("k_pages and v_pages must be 4-D and alike")
-    if k_pages.stride() != v_pages.stride() or k_pages.stride(3) != 1:
-        raise ValueError("k_pages and v_pages must share strides, the last one 1")
-    P, a, b, d = k_pages.shape
-    sp, sa, sb, _ = k_pages.stride()
-    page, H, st, sh = (b, a, sb, sa) if head_major else (a, b, sa, sb)
-    return ((k_pages.data_ptr(), v_pages.data_ptr(), sp, st, sh, P, page, _dtype_code(k_pages)),
-            (H, d))
-
-
-def _paged_workspace(workspace, need, device):
-    """(workspace kept alive, pointer, bytes)."""
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
 
 def gret_paged_status(status):
     """Synchronise and return the GRET_PAGED_* bits that paged calls left in their status word
@@ -511,30 +459,8 @@ def gret_paged_attention_decode(q, seq_lens, page_table, k_pages, v_pages, windo
     [P, page, Hkv, d], or [P, Hkv, page, d] with head_major; seq_lens int32 [B] and page_table int32
     [B, max_pages] on the device.  scale defaults to d^-1/2.  Sequences of length 0 give zeros.
     Returns (o [B, Hq, d], lse); lse=True allocates the log-sum-exp fp32 [B, Hq], None skips it."""
-    B, Hq, d = q.shape
-    pool, (Hkv, dp) = _paged_pool(k_pages, v_pages, head_major)
-    if d != dp or q.dtype != k_pages.dtype or not q.is_contiguous():
-        raise ValueError("q must be contiguous [B, Hq, d] with the pool's d and dtype")
-    table = _paged_table(page_table, B)
-    with _paged_scope(q.device, stream, (seq_lens, page_table, k_pages, v_pages, o, status, workspace,
-                                         None if lse is True else lse)):
-        if o is None:
-            o = torch.empty_like(q)
-        elif o.shape != q.shape or o.dtype != q.dtype or not o.is_contiguous():
-            raise ValueError("o must be contiguous and of q's shape and dtype")
-        if lse is True:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-        elif lse is not None and (lse.shape != (B, Hq) or lse.dtype != torch.float32
-                                  or not lse.is_contiguous()):
-            raise ValueError("lse must be contiguous float32 [B, Hq]")
-        workspace, ws, ws_bytes = _paged_workspace(
-            workspace, _lib.gret_paged_attention_workspace_size(pool[7], Hq, Hkv, d), q.device)
-        _check("gret_paged_attention_decode", _lib.gret_paged_attention_decode(
-            q.data_ptr(), _int32(seq_lens, "seq_lens", B), *table, *pool,
-            d ** -0.5 if scale is None else scale, window, B, Hq, Hkv, d, o.data_ptr(),
-            None if lse is None else lse.data_ptr(), _int32(status, "status", 1), ws, ws_bytes,
-            _stream(None)))
-    return o, lse
+    return _paged.attention_decode(q, seq_lens, page_table, k_pages, v_pages, window, scale,
+                                   head_major, o, lse, status, workspace, stream)
 
 
 def gret_paged_append(k, v, pos, page_table, k_pages, v_pages, cu_seqlens=None, head_major=False,
@@ -544,19 +470,8 @@ def gret_paged_append(k, v, pos, page_table, k_pages, v_pages, cu_seqlens=None, 
     i goes to position pos[i] of row i.  Rows with pos < 0 are skipped.  pos int32 [S] is what
     gret_paged_resize returns; page_table int32 [S, max_pages]; the pool as in
     gret_paged_attention_decode, updated in place."""
-    T, H, d = k.shape
-    pool, heads = _paged_pool(k_pages, v_pages, head_major)
-    if (H, d) != heads or v.shape != k.shape or k.dtype != k_pages.dtype or v.dtype != k.dtype:
-        raise ValueError("k and v must be [T, Hkv, d] with the pool's heads and dtype")
-    if k.stride(2) != 1 or v.stride(2) != 1:
-        raise ValueError("last dimension must be contiguous")
-    S = pos.numel()
-    table = _paged_table(page_table, S)
-    with _paged_scope(k.device, stream, (v, pos, page_table, k_pages, v_pages, cu_seqlens, status)):
-        _check("gret_paged_append", _lib.gret_paged_append(
-            k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), T,
-            _int32(cu_seqlens, "cu_seqlens", S + 1), _int32(pos, "pos", S), S, *table, *pool, H, d,
-            _int32(status, "status", 1), _stream(None)))
+    return _paged.append(k, v, pos, page_table, k_pages, v_pages, cu_seqlens, head_major, status,
+                         stream)
 
 
 def gret_paged_resize_workspace_size(S):
@@ -571,21 +486,8 @@ def gret_paged_resize(delta, seq_lens, page_table, ref, k_pages, v_pages, head_m
     max_pages], ref int32 [P]; all but delta, and the pool, are updated in place.  Returns pos
     int32 [S]: a grown row's old length, where its new tokens go, and -1 for the others (among them
     rows refused because the pool or the table is full, which stay as they are)."""
-    S = seq_lens.numel()
-    pool, (H, d) = _paged_pool(k_pages, v_pages, head_major)
-    table = _paged_table(page_table, S)
-    device = seq_lens.device
-    with _paged_scope(device, stream, (delta, page_table, ref, k_pages, v_pages, pos, status,
-                                       workspace)):
-        if pos is None:
-            pos = torch.empty(S, dtype=torch.int32, device=device)
-        workspace, ws, ws_bytes = _paged_workspace(
-            workspace, _lib.gret_paged_resize_workspace_size(S), device)
-        _check("gret_paged_resize", _lib.gret_paged_resize(
-            _int32(delta, "delta", S), _int32(seq_lens, "seq_lens", S), S, *table,
-            _int32(ref, "ref", pool[5]), *pool, H, d, _int32(pos, "pos", S),
-            _int32(status, "status", 1), ws, ws_bytes, _stream(None)))
-    return pos
+    return _paged.resize(delta, seq_lens, page_table, ref, k_pages, v_pages, head_major, pos, status,
+                         workspace, stream)
 
 
 def gret_paged_fork(src, dst, seq_lens, page_table, ref, page_size, status=None, stream=None):
@@ -594,13 +496,7 @@ def gret_paged_fork(src, dst, seq_lens, page_table, ref, page_size, status=None,
     empty rows, no row is a source and a destination, none is a destination twice (such pairs
     are left out).  seq_lens int32 [S], page_table int32 [S, max_pages] and ref int32 [P] are updated in
     place.  The rows part ways when gret_paged_resize grows them."""
-    S, n = seq_lens.numel(), src.numel()
-    table = _paged_table(page_table, S)
-    with _paged_scope(seq_lens.device, stream, (src, dst, page_table, ref, status)):
-        _check("gret_paged_fork", _lib.gret_paged_fork(
-            _int32(src, "src", n), _int32(dst, "dst", n), n, _int32(seq_lens, "seq_lens", S), S,
-            *table, _int32(ref, "ref", ref.numel()), ref.numel(), page_size,
-            _int32(status, "status", 1), _stream(None)))
+    return _paged.fork(src, dst, seq_lens, page_table, ref, page_size, status, stream)
 
 
 def gret_paged_compact_workspace_size(n_pages):
@@ -612,17 +508,5 @@ def gret_paged_compact(seq_lens, page_table, ref, k_pages, v_pages, head_major=F
     """Move the L pages in use (ref > 0) to the pages [0, L) of the pool; ref int32 [P] and
     page_table int32 [S, max_pages] follow, in place.  Returns n_live int32 [1] = L: pages from L on
     are free."""
-    S = seq_lens.numel()
-    pool, (H, d) = _paged_pool(k_pages, v_pages, head_major)
-    table = _paged_table(page_table, S)
-    device = seq_lens.device
-    with _paged_scope(device, stream, (page_table, ref, k_pages, v_pages, n_live, status,
-                                       workspace)):
-        if n_live is None:
-            n_live = torch.empty(1, dtype=torch.int32, device=device)
-        workspace, ws, ws_bytes = _paged_workspace(
-            workspace, _lib.gret_paged_compact_workspace_size(pool[5]), device)
-        _check("gret_paged_compact", _lib.gret_paged_compact(
-            _int32(seq_lens, "seq_lens", S), S, *table, _int32(ref, "ref", pool[5]), *pool, H, d,
-            _int32(n_live, "n_live", 1), _int32(status, "status", 1), ws, ws_bytes, _stream(None)))
-    return n_live
+    return _paged.compact(seq_lens, page_table, ref, k_pages, v_pages, head_major, n_live, status,
+                          workspace, stream)

@@ -1,4 +1,5 @@
-"""Build libgret.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc.
+"""Build libgret.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and with g++ _paged.so,
+the Python side of the paged cache's calls, against it and the installed torch.
 
     python gated_retention_linear_b200/build.py [--force] [--verbose]
 
@@ -11,15 +12,18 @@ time through the runtime, so the library does not link libcuda.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgret.so")
+BINDING = os.path.join(PKG, "_paged.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -48,6 +52,22 @@ def _compile(src, verbose):
     return obj, r.stderr
 
 
+def _build_binding(force):
+    src = os.path.join(CSRC, "paged_binding.cpp")
+    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "gret.h")]):
+        return
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = [os.path.join(torch, "include"), sysconfig.get_paths()["include"], INCLUDE,
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-fPIC", "-shared",
+                    "-fvisibility=hidden"] + ["-I" + i for i in inc]
+                   + [src, "-o", tmp, "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+                      "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB),
+                      "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -64,6 +84,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    _build_binding(force)
     return LIB
 
 
