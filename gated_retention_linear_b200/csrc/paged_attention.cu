@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
     unsigned char* ring = smem + warp * RING;
     unsigned char* qs = smem + NW * RING;
     unsigned char* scratch = qs + M::QBYTES + warp * M::SCRATCH;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_previous();
+    let_next_start();
     Segment seg;
     int64_t b_unit;
     const Deal deal = deal_of(p, blockIdx.x, false, deal_smem, seg.b, b_unit);
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
         rows = min(M::ROWS, p.G - pr % p.QG * M::ROWS);
     }
     // every block waits: the end of this kernel is to mean the end of both
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_previous();
     if (n == 0 || r >= rows) return;
     const int64_t head = (int64_t)b * p.Hq + row0 + r;
     const Part<M::ROWS, D>* parts = static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c;
@@ -784,19 +785,10 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<M>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    paged_attn_kernel<M><<<GRID, NT, smem, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_early(paged_attn_kernel<M>, dim3(GRID), NT, smem, stream, p);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(GRID, M::ROWS < p.G ? M::ROWS : p.G);
-    cfg.blockDim = dim3(NT);
-    cfg.stream = stream;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<M>, static_cast<const Params&>(p));
+    return launch_early(paged_join_kernel<M>, dim3(GRID, M::ROWS < p.G ? M::ROWS : p.G), NT, 0,
+                        stream, p);
 }
 
 // Query rows a block works on at a time: all G heads of a group where they fit, else the fewest

@@ -219,32 +219,6 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-// Launch a kernel that may start before the one launched last has ended; it waits for that end
-// itself (wait_for_plan).
-template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), int blocks, int threads, size_t smem,
-                             cudaStream_t stream, const Args&... args) {
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-__device__ __forceinline__ void let_dependents_start() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-__device__ __forceinline__ void wait_for_plan() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // ---------------------------------------------------------------------------------------------
 // append: a copy of every token's row of heads to its slot.  Bound by HBM, each byte read and
 // written once; with few tokens by the chain row -> position -> page -> copy, so a warp's lanes
@@ -270,6 +244,7 @@ __device__ __forceinline__ int row_of(const int32_t* cu, int S, int64_t i) {
 
 __global__ void __launch_bounds__(NT) append_kernel(const PagedAppendArgs a, const FastDiv token,
                                                     const FastDiv row, const int tok) {
+    wait_for_previous();
     const int lane = threadIdx.x & 31;
     const int64_t i0 = ((int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5)) * tok;
     if (i0 >= a.T) return;
@@ -367,7 +342,8 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     int* first = rows_smem + a.table.S;           // [S] table entry the first of them goes to
     cg::cluster_group cluster = cg::this_cluster();
     cluster.barrier_arrive();
-    let_dependents_start();
+    wait_for_previous();
+    let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, S = a.table.S;
     const bool lead = cluster.block_rank() == 0;
     const int shift = a.pool.page_shift;
@@ -520,7 +496,7 @@ __global__ void __launch_bounds__(NT) resize_apply_kernel(const PagedResizeArgs 
                                                           const Pieces pc) {
     __shared__ int from[NT], to[NT], slots[NT], copies;
     const int tid = threadIdx.x, S = a.table.S, shift = a.pool.page_shift;
-    wait_for_plan();
+    wait_for_previous();
     // a block a row: pages that it drops, its new length
     for (int s = blockIdx.x; s < S; s += GRID) {
         const Change c = change_of(a, s);
@@ -596,7 +572,8 @@ __global__ void __launch_bounds__(NT) fork_kernel(const PagedForkArgs a) {
     extern __shared__ int first[];
     __shared__ int before[NT / 32], siblings[NT / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (SHARE) let_dependents_start();
+    wait_for_previous();
+    if (SHARE) let_next_start();
     first_pairs(a, first);
     for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
         if (!takes_effect(a, first, i)) {
@@ -663,7 +640,7 @@ __global__ void __launch_bounds__(NT) fork_lengths_kernel(const PagedForkArgs a)
     first_pairs(a, first);
     const int i = blockIdx.x * NT + threadIdx.x;
     const bool ok = i < a.n && takes_effect(a, first, i);
-    wait_for_plan();
+    wait_for_previous();
     if (ok) a.seq_lens[a.dst[i]] = a.seq_lens[a.src[i]];
 }
 
@@ -687,7 +664,8 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     __shared__ int chunk_before[MAXCH];
     cg::cluster_group cluster = cg::this_cluster();
     cluster.barrier_arrive();
-    let_dependents_start();
+    wait_for_previous();
+    let_next_start();
     const int lane = threadIdx.x & 31, P = a.pool.n_pages;
     const CompactPlan plan = compact_plan(a);
     count_free(a.ref, P, chunk_before);
@@ -734,7 +712,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
 __global__ void __launch_bounds__(NT) compact_move_kernel(const PagedCompactArgs a,
                                                           const Pieces pc) {
     const CompactPlan plan = compact_plan(a);
-    wait_for_plan();
+    wait_for_previous();
     const int L = plan.counts[0], moves = plan.counts[1];
     // step c of move k, dealt over the blocks.  The counts move apart from the pages: a thread that
     // waits for a count inside this loop holds its block's next step up (332 -> 388 us for 16448
@@ -787,19 +765,17 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
     const int tok = (int)(even < 1 ? 1 : even > AP_MAXTOK ? AP_MAXTOK : even);
     const int64_t per = (int64_t)(NT / 32) * tok;
     const uint32_t row = a.pool.row_bytes / 16;
-    append_kernel<<<(unsigned)((a.T + per - 1) / per), NT, 0, stream>>>(
-        a, FastDiv(a.pool.H * row), FastDiv(row), tok);
-    return cudaGetLastError();
+    return launch_early(append_kernel, dim3((unsigned)((a.T + per - 1) / per)), NT, 0, stream, a,
+                        FastDiv(a.pool.H * row), FastDiv(row), tok);
 }
 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)a.table.S * 2 * sizeof(int);
     cudaError_t e = allow_smem(resize_plan_kernel, smem);
     if (e != cudaSuccess) return e;
-    resize_plan_kernel<<<CL, PNT, smem, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(resize_plan_kernel, dim3(CL), PNT, smem, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_dependent(resize_apply_kernel, GRID, NT, 0, stream, a, Pieces(a.pool));
+    return launch_early(resize_apply_kernel, dim3(GRID), NT, 0, stream, a, Pieces(a.pool));
 }
 
 cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
@@ -811,8 +787,7 @@ cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
     if (a.table.max_pages <= 4096 && (int64_t)a.n * a.table.max_pages <= FORK_ALONE) {
         e = allow_smem(fork_kernel<false>, smem);
         if (e != cudaSuccess) return e;
-        fork_kernel<false><<<x, NT, smem, stream>>>(a);
-        return cudaGetLastError();
+        return launch_early(fork_kernel<false>, dim3(x), NT, smem, stream, a);
     }
     e = allow_smem(fork_kernel<true>, smem);
     if (e == cudaSuccess) e = allow_smem(fork_lengths_kernel, smem);
@@ -820,17 +795,15 @@ cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
     // a block a pair; with few pairs a row is cut up, in pieces of 1024 entries at least
     int y = 2 * GRID / x, most = (a.table.max_pages + 1023) / 1024;
     if (y > most) y = most;
-    fork_kernel<true><<<dim3(x, y), NT, smem, stream>>>(a);
-    e = cudaGetLastError();
+    e = launch_early(fork_kernel<true>, dim3(x, y), NT, smem, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_dependent(fork_lengths_kernel, (a.n + NT - 1) / NT, NT, smem, stream, a);
+    return launch_early(fork_lengths_kernel, dim3((a.n + NT - 1) / NT), NT, smem, stream, a);
 }
 
 cudaError_t launch_paged_compact(const PagedCompactArgs& a, cudaStream_t stream) {
-    compact_plan_kernel<<<CL, PNT, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(compact_plan_kernel, dim3(CL), PNT, 0, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_dependent(compact_move_kernel, GRID, NT, 0, stream, a, Pieces(a.pool));
+    return launch_early(compact_move_kernel, dim3(GRID), NT, 0, stream, a, Pieces(a.pool));
 }
 
 }  // namespace gret
