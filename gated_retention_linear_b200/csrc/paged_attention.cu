@@ -29,6 +29,7 @@
 // a second kernel joins the parts in block order, so that results do not depend on timing.  It is
 // launched as a dependent of the first one, whose end it waits for on the device.
 #include <cuda_bf16.h>
+#include <limits.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -41,13 +42,16 @@ namespace {
 
 constexpr int NT = 128;
 constexpr int NW = NT / 32;
-constexpr int UNIT = 64;               // keys of one unit of work
+constexpr int UNIT = 32;               // keys of one unit of work
 constexpr int S = 3;                   // tiles of a warp's ring
 constexpr int HALF = 4096;             // bytes of a tile's keys, and of its values
 constexpr int RING = S * 2 * HALF;
 constexpr int MAXROWS = 32;            // query rows a block works on at a time
 constexpr int BLOCKS_SM = 2;           // 2 x (4 rings of 24 KB + queries) fill an SM's 227 KB
 constexpr int GRID = 148 * BLOCKS_SM;
+constexpr int JOIN_NT = 128;
+constexpr int JOIN_NW = JOIN_NT / 32;
+constexpr int JOIN_Y = 8;              // blocks a pair of the join: 8 x GRID find room at once
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -277,7 +281,8 @@ struct F32Math {
     static constexpr int QROW = D / 32 * 144;
     static constexpr int QBYTES = R * QROW, SCRATCH = KT * R * 4, NPASS = 1;
 
-    float m[R], l[R], acc[R][4];
+    float m[R], l[R];
+    float2 acc[R][2];            // dimensions 4 (lane % CPR) and on
 
     __device__ static __forceinline__ int q_place(int r, int c) {
         return r * QROW + c / 8 * 144 + c % 8 * 16;
@@ -288,8 +293,7 @@ struct F32Math {
         for (int r = 0; r < R; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[r][e] = 0.f;
+            acc[r][0] = acc[r][1] = make_float2(0.f, 0.f);
         }
     }
 
@@ -297,9 +301,10 @@ struct F32Math {
                                          const unsigned char* qs, unsigned char* scratch,
                                          unsigned ok, float scale, int lane) {
         const int key = lane % KT, part = lane / KT;       // this lane's 32 of the D dimensions
+        float2 s2[R];                                      // even and odd dimensions
         float s[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r] = 0.f;
+        for (int r = 0; r < R; ++r) s2[r] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const float4 k = *reinterpret_cast<const float4*>(
@@ -308,7 +313,8 @@ struct F32Math {
             for (int r = 0; r < R; ++r) {
                 const float4 q =
                     *reinterpret_cast<const float4*>(qs + r * QROW + part * 144 + c * 16);
-                s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+                s2[r] = sm100::fma2(make_float2(q.x, q.y), make_float2(k.x, k.y), s2[r]);
+                s2[r] = sm100::fma2(make_float2(q.z, q.w), make_float2(k.z, k.w), s2[r]);
             }
         }
         const bool okk = ok >> key & 1;
@@ -316,6 +322,7 @@ struct F32Math {
         bool up = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            s[r] = s2[r].x + s2[r].y;
 #pragma unroll
             for (int o = KT; o < 32; o <<= 1) s[r] += __shfl_xor_sync(~0u, s[r], o);
             s[r] = okk ? s[r] * scale : -INFINITY;
@@ -331,8 +338,8 @@ struct F32Math {
                 const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn[r]);
                 l[r] *= f;
                 m[r] = mn[r];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[r][e] *= f;
+                acc[r][0] = sm100::mul2(acc[r][0], make_float2(f, f));
+                acc[r][1] = sm100::mul2(acc[r][1], make_float2(f, f));
             }
         }
         float* pk = reinterpret_cast<float*>(scratch);     // [KT][R]
@@ -359,10 +366,9 @@ struct F32Math {
                 const float pr[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    acc[r + e][0] = fmaf(pr[e], v.x, acc[r + e][0]);
-                    acc[r + e][1] = fmaf(pr[e], v.y, acc[r + e][1]);
-                    acc[r + e][2] = fmaf(pr[e], v.z, acc[r + e][2]);
-                    acc[r + e][3] = fmaf(pr[e], v.w, acc[r + e][3]);
+                    const float2 pp = make_float2(pr[e], pr[e]);
+                    acc[r + e][0] = sm100::fma2(pp, make_float2(v.x, v.y), acc[r + e][0]);
+                    acc[r + e][1] = sm100::fma2(pp, make_float2(v.z, v.w), acc[r + e][1]);
                 }
             }
         }
@@ -383,12 +389,13 @@ struct F32Math {
     __device__ __forceinline__ void put(int, float* to, int lane) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
+            float x[4] = {acc[r][0].x, acc[r][0].y, acc[r][1].x, acc[r][1].y};
             if (KI == 2)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[r][e] += __shfl_xor_sync(~0u, acc[r][e], 16);
+                for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(~0u, x[e], 16);
             if (lane < CPR)
                 *reinterpret_cast<float4*>(to + r * (D + 4) + 4 * lane) =
-                    make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+                    make_float4(x[0], x[1], x[2], x[3]);
         }
     }
 };
@@ -415,11 +422,19 @@ __device__ __forceinline__ int units_of(const Params& p, int b) {
     return units_between(first, len);
 }
 
-// A stretch of one pair's units that a block works on: units [t0, t1) of nu.
+// What ending a pair costs, in units: 0.8 us for each 8 rows, when a block reads 22 KB a us.
+template <class M>
+constexpr int end_units() {
+    constexpr int unit_ns = UNIT * 2 * M::ROWB * 1000 / 22000, end_ns = 800 * M::NPASS;
+    return (end_ns + unit_ns / 2) / unit_ns < 1 ? 1 : (end_ns + unit_ns / 2) / unit_ns;
+}
+
+// A stretch of one pair's units that a block works on: units [t0, t1) of the nu that hold keys;
+// `last` units for the pair's end follow those in the count.
 struct Segment {
     int64_t u;                   // of the whole batch's units, the one t0 stands for
     uint32_t first, len;
-    int b, pr, nu, t0, t1;
+    int b, pr, nu, t0, t1, last;
 
     __device__ __forceinline__ uint32_t key0() const { return first + (uint32_t)t0 * UNIT; }
     __device__ __forceinline__ uint32_t key1() const {
@@ -427,7 +442,7 @@ struct Segment {
     }
     // To the next one of a block whose units end before u1.
     __device__ __forceinline__ bool next(const Params& p, int64_t u1) {
-        u += t1 - t0;
+        u += nu + last - t0;
         if (u >= u1) return false;
         t0 = 0;                  // only a block's last segment ends inside its pair
         if (++pr == p.pool.H * p.QG) {
@@ -443,33 +458,58 @@ struct Segment {
     }
 };
 
-// How the batch's U units are dealt: `blocks` blocks, block c has units [U c / blocks,
-// U (c + 1) / blocks).  With fewer units than blocks, the first U blocks take one each: a pair's
-// parts lie in consecutive blocks.
+// How the batch's U units are dealt: block c has units [begin(c), begin(c + 1)), each of the first
+// `more` blocks one more than the others' `each`.  With fewer units than blocks, the first U blocks
+// take one each: a pair's parts lie in consecutive blocks.  A pair counts for more units than its
+// keys fill, since ending one (joining the warps' parts, writing the outcome) takes time too:
+// counted by keys alone, blocks of many short pairs came last.
 struct Deal {
-    int64_t U, blocks;
+    int64_t U, each;
+    int more;
 
-    __device__ __forceinline__ int64_t begin(int64_t c) const { return U * c / blocks; }
-    // The block that holds unit x is the largest c with floor(c U / blocks) <= x.
+    __device__ __forceinline__ explicit Deal(int64_t units)
+        : U(units), each(units / GRID), more((int)(units % GRID)) {}
+    __device__ __forceinline__ int64_t begin(int c) const { return each * c + min(c, more); }
+    // The block that holds unit x.
     __device__ __forceinline__ int block_of(int64_t x) const {
-        return (int)(((x + 1) * blocks - 1) / U);
+        const int64_t head = (each + 1) * more;
+        return x < head ? (int)(x / (each + 1)) : more + (int)((x - head) / each);
     }
 };
 
+// x = pr * nu + t: most often in 32 bits, which take a fifth of the time of a division in 64.
+__device__ __forceinline__ void pair_of(int64_t x, int nu, int& pr, int& t) {
+    if (x <= INT_MAX) {
+        pr = (int)x / nu;
+        t = (int)x % nu;
+    } else {
+        pr = (int)(x / nu);
+        t = (int)(x % nu);
+    }
+}
+
 struct DealSmem {
-    int64_t scan[NT / 32], unit;
+    int64_t scan[JOIN_NW], unit;
     int b;
 };
 
+// Units that sequence b is dealt as: of each pair its keys' and those of its end.
+template <class M>
+__device__ __forceinline__ int64_t dealt_units(const Params& p, int b) {
+    const int nu = units_of(p, b);
+    return nu ? (int64_t)(nu + end_units<M>()) * (p.pool.H * p.QG) : 0;
+}
+
 // The deal, and the place of the first (`last`: the last) unit of block c: its sequence b, and
 // the first unit of that.  Called by all NT threads; without units for block c, b = -1.
+template <class M, int NT>
 __device__ __forceinline__ Deal deal_of(const Params& p, int c, bool last, DealSmem& sm, int& b,
                                         int64_t& unit) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int B = p.table.S, pairs_b = p.pool.H * p.QG, per = (B + NT - 1) / NT;
+    const int B = p.table.S, per = (B + NT - 1) / NT;
     const int b1 = min(B, (tid + 1) * per);
     int64_t mine = 0;
-    for (int i = tid * per; i < b1; ++i) mine += (int64_t)units_of(p, i) * pairs_b;
+    for (int i = tid * per; i < b1; ++i) mine += dealt_units<M>(p, i);
     int64_t incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(~0u, incl, o);
@@ -477,23 +517,21 @@ __device__ __forceinline__ Deal deal_of(const Params& p, int c, bool last, DealS
     }
     if (lane == 31) sm.scan[warp] = incl;
     __syncthreads();
-    Deal d;
-    d.U = 0;
-    int64_t before = incl - mine;
+    int64_t U = 0, before = incl - mine;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) before += sm.scan[w];
-        d.U += sm.scan[w];
+        U += sm.scan[w];
     }
-    d.blocks = min(d.U, (int64_t)GRID);
+    const Deal d(U);
     b = -1;
     unit = 0;
-    if (c >= d.blocks) return d;
+    if (c >= U) return d;
     const int64_t u = last ? d.begin(c + 1) - 1 : d.begin(c);
     if (before <= u && u < before + mine) {
         int64_t at = before;
         for (int i = tid * per; i < b1; ++i) {
-            const int64_t x = (int64_t)units_of(p, i) * pairs_b;
+            const int64_t x = per == 1 ? mine : dealt_units<M>(p, i);
             if (u < at + x) {
                 sm.b = i;
                 sm.unit = at;
@@ -525,66 +563,17 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
     let_next_start();
     Segment seg;
     int64_t b_unit;
-    const Deal deal = deal_of(p, blockIdx.x, false, deal_smem, seg.b, b_unit);
+    const Deal deal = deal_of<M, NT>(p, blockIdx.x, false, deal_smem, seg.b, b_unit);
     if (seg.b < 0) return;
     const int64_t u0 = deal.begin(blockIdx.x), u1 = deal.begin(blockIdx.x + 1);
     key_range(p, seg.b, seg.first, seg.len);
     seg.nu = units_between(seg.first, seg.len);
     seg.u = u0;
-    seg.pr = (int)((u0 - b_unit) / seg.nu);
-    seg.t0 = (int)((u0 - b_unit) % seg.nu);
+    seg.last = end_units<M>();
+    pair_of(u0 - b_unit, seg.nu + seg.last, seg.pr, seg.t0);
     seg.t1 = (int)min((int64_t)seg.nu, seg.t0 + (u1 - u0));
-
-    // The tile to load next.  Its page-table entries are read when it becomes that, a whole tile's
-    // work before they are needed.
-    Segment ls = seg;
-    uint32_t at = ls.key0() + warp * KT, end = ls.key1();
-    bool more = true;
-    int id = 0;
-    const int page_shift = p.pool.page_shift;
-    auto look_up = [&]() {
-        while (more && at >= end) {
-            more = ls.next(p, u1);
-            at = ls.key0() + warp * KT;
-            end = ls.key1();
-        }
-        if (more && lane < KT && at + lane < end)
-            id = p.table.entries[ls.b * p.table.stride + ((at + lane) >> page_shift)];
-    };
-    // Load it, and go on to the next: a bit for every key that counts.
-    auto load = [&](int stage) {
-        unsigned ok = 0;
-        if (more) {
-            const bool in = lane < KT && at + lane < end;
-            const bool good = in && (unsigned)id < (unsigned)p.pool.n_pages;
-            if (in && !good) paged_flag(p.status, GRET_PAGED_BAD_PAGE);
-            ok = __ballot_sync(~0u, good);
-            const int64_t off = !good ? 0
-                                      : id * p.pool.sp +
-                                            ((at + lane) & ((1u << page_shift) - 1)) * p.pool.st +
-                                            ls.pr / p.QG * p.pool.sh;
-            const uint32_t to = sm100::smem_u32(ring + stage * 2 * HALF);
-            const int c = lane % CPR;
-            at += NW * KT;
-            look_up();
-#pragma unroll
-            for (int i = 0; i < KT * CPR / 32; ++i) {
-                const int r = i * (32 / CPR) + lane / CPR;
-                const int64_t o = __shfl_sync(~0u, off, r) + c * 16;
-                const uint32_t dst = to + r * ROWB + ((c ^ (r & 7)) << 4);
-                const uint32_t bytes = ok >> r & 1 ? 16 : 0;
-                cp_async_16_or_zero(dst, p.pool.k + o, bytes);
-                cp_async_16_or_zero(dst + HALF, p.pool.v + o, bytes);
-            }
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        return ok;
-    };
-    unsigned ok[S];
-    look_up();
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) ok[i] = load(i);
-    int stage = 0;
+    // a range that begins among the units of an end, and maybe holds nothing else
+    if (seg.t0 >= seg.nu && !seg.next(p, u1)) return;
 
     // A segment's queries: read one segment ahead, put into shared memory when it begins.
     uint4 qn[QC];
@@ -608,6 +597,70 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         }
     };
     read_q(seg);
+
+    // The tiles to load next.  A tile's page-table entries are read when it enters this queue, two
+    // tiles before they are needed: one latency for all of a ring's first tiles.
+    struct Tile {
+        int64_t head;            // bytes from a slot to its head's row
+        uint32_t at, end;        // its first key, and the end of its segment (at >= end: no tile)
+        int id;                  // of lane's key: its page
+    };
+    Tile ahead[S - 1] = {};
+    Segment ls = seg;
+    uint32_t at = ls.key0() + warp * KT, end = ls.key1();
+    bool more = true;
+    const int page_shift = p.pool.page_shift;
+    auto look_up = [&](Tile& t) {
+        while (more && at >= end) {
+            more = ls.next(p, u1);
+            at = ls.key0() + warp * KT;
+            end = ls.key1();
+        }
+        t.at = at;
+        t.end = more ? end : 0;
+        t.head = ls.pr / p.QG * p.pool.sh;
+        t.id = -1;
+        if (lane < KT && at + lane < t.end)
+            t.id = p.table.entries[ls.b * p.table.stride + ((at + lane) >> page_shift)];
+        at += NW * KT;
+    };
+    // Load the first of them, and take up another: a bit for every key that counts.
+    auto load = [&](int stage) {
+        const Tile t = ahead[0];
+        unsigned ok = 0;
+        if (t.at < t.end) {
+            const bool in = lane < KT && t.at + lane < t.end;
+            const bool good = in && (unsigned)t.id < (unsigned)p.pool.n_pages;
+            if (in && !good) paged_flag(p.status, GRET_PAGED_BAD_PAGE);
+            ok = __ballot_sync(~0u, good);
+            const int64_t off = good ? t.id * p.pool.sp +
+                                           ((t.at + lane) & ((1u << page_shift) - 1)) * p.pool.st +
+                                           t.head
+                                     : 0;
+#pragma unroll
+            for (int i = 0; i < S - 2; ++i) ahead[i] = ahead[i + 1];
+            look_up(ahead[S - 2]);
+            const uint32_t to = sm100::smem_u32(ring + stage * 2 * HALF);
+            const int c = lane % CPR;
+#pragma unroll
+            for (int i = 0; i < KT * CPR / 32; ++i) {
+                const int r = i * (32 / CPR) + lane / CPR;
+                const int64_t o = __shfl_sync(~0u, off, r) + c * 16;
+                const uint32_t dst = to + r * ROWB + ((c ^ (r & 7)) << 4);
+                const uint32_t bytes = ok >> r & 1 ? 16 : 0;
+                cp_async_16_or_zero(dst, p.pool.k + o, bytes);
+                cp_async_16_or_zero(dst + HALF, p.pool.v + o, bytes);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return ok;
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) look_up(ahead[i]);
+    unsigned ok[S];
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) ok[i] = load(i);
+    int stage = 0;
     put_q();
     __syncthreads();
 
@@ -636,19 +689,21 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nu;
         Part<M::ROWS, D>* part =
             static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * blockIdx.x + (seg.t0 == 0);
-        float* mine_put =
-            reinterpret_cast<float*>(ring + (stage == 0 ? S - 1 : stage - 1) * 2 * HALF);
+        // a pass a tile of rows; when the block ends here, nothing is under way, and one pass does
+        constexpr int PR = M::ROWS / M::NPASS;             // rows of a tile
+        const int np = go ? 1 : M::NPASS;
+        float* mine_put = reinterpret_cast<float*>(
+            ring + (go ? (stage == 0 ? S - 1 : stage - 1) * 2 * HALF : 0));
         if (lane == 0) wput[warp] = mine_put;
         math.end(wm[warp], wl[warp], lane);
-#pragma unroll
-        for (int pass = 0; pass < M::NPASS; ++pass) {
-            constexpr int PR = M::ROWS / M::NPASS;         // rows of a pass
-            math.put(pass, mine_put, lane);
+#pragma unroll 1
+        for (int pass = 0; pass < M::NPASS; pass += np) {
+            for (int i = 0; i < np; ++i) math.put(pass + i, mine_put + i * PR * (D + 4), lane);
             __syncthreads();
             if (pass == 0 && go) put_q();
-            for (int i = tid; i < PR * D / 4; i += NT) {
-                const int r = i / (D / 4), e = i % (D / 4) * 4, row = pass * PR + r;
-                if (row >= rows) break;
+            const int row0 = pass * PR, n = min(rows - row0, np * PR);
+            for (int i = tid; i < n * (D / 4); i += NT) {
+                const int r = i / (D / 4), e = i % (D / 4) * 4, row = row0 + r;
                 float mx = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w][row]);
@@ -678,86 +733,66 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
                     }
                 }
             }
-            __syncthreads();
+            if (go) __syncthreads();
         }
         seg = nx;
     }
 }
 
-// Block (c, r) joins row r of the parts of the pair that block c of the kernel above began and
-// did not finish: a warp a quarter of the parts, a lane D / 32 dimensions.  Which pair that is
-// follows from the lengths, so this kernel finds it out while the other is still at work.
+// Row r of the n parts, to query row `head`: a warp a quarter of the parts, a lane D / 32 dimensions.  All
+// that a row is made of is on its way before any of it is looked at, up to 32 parts.  The block is small
+// so that it finds registers beside the kernel above's, and its deal is done while that one runs.
 template <class M>
-__global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
+__device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M::D>* parts, int n,
+                                         int r, int64_t head) {
     using T = typename M::T;
-    constexpr int D = M::D, E = D / 32, UN = 8;
-    __shared__ DealSmem deal_smem;
-    __shared__ float w[GRID];            // the parts' maxima, then their weights
-    __shared__ float sums[NW][D], red[2][NW];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = blockIdx.y, c = blockIdx.x;
-    // sequences without keys: zeros
-    for (int b = c; b < p.table.S; b += GRID)
-        if (units_of(p, b) == 0)
-            for (int i = r; i < p.Hq; i += gridDim.y) {
-                for (int e = tid; e < D; e += NT)
-                    static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * D + e] = from_f32<T>(0.f);
-                if (p.lse && tid == 0) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
-            }
-    int b;
-    int64_t b_unit;
-    const Deal deal = deal_of(p, c, true, deal_smem, b, b_unit);
-    int n = 0, row0 = 0, rows = 0;                         // parts; their first query row, rows
-    if (b >= 0) {
-        const int64_t u0 = deal.begin(c), u1 = deal.begin(c + 1);
-        const int nu = units_of(p, b), pr = (int)((u1 - 1 - b_unit) / nu);
-        const int64_t pair0 = b_unit + (int64_t)pr * nu;   // the pair's first unit
-        if (pair0 >= u0 && pair0 + nu > u1) n = deal.block_of(pair0 + nu - 1) - c + 1;
-        row0 = pr / p.QG * p.G + pr % p.QG * M::ROWS;
-        rows = min(M::ROWS, p.G - pr % p.QG * M::ROWS);
-    }
-    // every block waits: the end of this kernel is to mean the end of both
-    wait_for_previous();
-    if (n == 0 || r >= rows) return;
-    const int64_t head = (int64_t)b * p.Hq + row0 + r;
-    const Part<M::ROWS, D>* parts = static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c;
+    constexpr int D = M::D, E = D / 32, UN = 8, PER = (GRID + JOIN_NT - 1) / JOIN_NT;
+    __shared__ float w[GRID];                              // the parts' weights
+    __shared__ float sums[JOIN_NW][D], red[2][JOIN_NW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // part k: the tail of block c, then the heads of those that follow
-    float x[UN][E];
+    float x[UN][E], m[PER], l[PER];
     auto fetch = [&](int k0) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int k = k0 + i * NW;
+            const int k = k0 + i * JOIN_NW;
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 x[i][e] = k < n ? parts[2 * k + (k == 0)].a[r][lane + 32 * e] : 0.f;
         }
     };
-    fetch(warp);                                           // on their way beside the maxima
-    float mx = -INFINITY;
-    for (int k = tid; k < n; k += NT) {
-        w[k] = parts[2 * k + (k == 0)].m[r];
-        mx = fmaxf(mx, w[k]);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int k = tid + i * JOIN_NT;
+        m[i] = k < n ? parts[2 * k + (k == 0)].m[r] : -INFINITY;
+        l[i] = k < n ? parts[2 * k + (k == 0)].l[r] : 0.f;
     }
+    fetch(warp);
+    float mx = m[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) mx = fmaxf(mx, m[i]);
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
     if (lane == 0) red[0][warp] = mx;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NW; ++i) mx = fmaxf(mx, red[0][i]);
+    for (int i = 0; i < JOIN_NW; ++i) mx = fmaxf(mx, red[0][i]);
     const float base = mx == -INFINITY ? 0.f : mx;
     float z = 0.f;
-    for (int k = tid; k < n; k += NT) {
-        const float f = ex2(w[k] - base);
-        w[k] = f;
-        z += f * parts[2 * k + (k == 0)].l[r];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const float f = ex2(m[i] - base);
+        if (tid + i * JOIN_NT < n) w[tid + i * JOIN_NT] = f;
+        z += f * l[i];
     }
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
     if (lane == 0) red[1][warp] = z;
     __syncthreads();
     float a[E] = {};
-    for (int k0 = warp; k0 < n; k0 += NW * UN) {
+    for (int k0 = warp; k0 < n; k0 += JOIN_NW * UN) {
         if (k0 != warp) fetch(k0);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int k = k0 + i * NW;
+            const int k = k0 + i * JOIN_NW;
             const float f = k < n ? w[k] : 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) a[e] = fmaf(f, x[i][e], a[e]);
@@ -768,14 +803,55 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
     __syncthreads();
     z = 0.f;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) z += red[1][i];
-    for (int e = tid; e < D; e += NT) {
+    for (int i = 0; i < JOIN_NW; ++i) z += red[1][i];
+    if (tid < D) {
         float y = 0.f;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) y += sums[i][e];
-        static_cast<T*>(p.o)[head * D + e] = from_f32<T>(y / z);
+        for (int i = 0; i < JOIN_NW; ++i) y += sums[i][tid];
+        static_cast<T*>(p.o)[head * D + tid] = from_f32<T>(y / z);
     }
     if (p.lse && tid == 0) p.lse[head] = (mx + log2f(z)) * LN2;
+}
+
+// Blocks (c, y) join the parts of the pair that block c of the kernel above began and did not
+// finish, each every JOIN_Y-th row.  Which pair that is follows from the lengths, so this kernel finds
+// it out while the other is still at work.
+template <class M>
+__global__ void __launch_bounds__(JOIN_NT) paged_join_kernel(const Params p) {
+    using T = typename M::T;
+    constexpr int D = M::D;
+    __shared__ DealSmem deal_smem;
+    const int tid = threadIdx.x, c = blockIdx.x;
+    // sequences without keys: zeros
+    for (int b = c; b < p.table.S; b += GRID)
+        if (units_of(p, b) == 0)
+            for (int i = blockIdx.y; i < p.Hq; i += gridDim.y) {
+                for (int e = tid; e < D; e += JOIN_NT)
+                    static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * D + e] = from_f32<T>(0.f);
+                if (p.lse && tid == 0) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
+            }
+    int b;
+    int64_t b_unit;
+    const Deal deal = deal_of<M, JOIN_NT>(p, c, true, deal_smem, b, b_unit);
+    int n = 0, row0 = 0, rows = 0;                         // parts; their first query row, rows
+    if (b >= 0) {
+        const int64_t u0 = deal.begin(c), u1 = deal.begin(c + 1);
+        const int nu = units_of(p, b);
+        int pr, t;
+        pair_of(u1 - 1 - b_unit, nu + end_units<M>(), pr, t);
+        const int64_t pair0 = u1 - 1 - t;                  // the pair's first unit
+        if (pair0 >= u0 && pair0 + nu > u1) n = deal.block_of(pair0 + nu - 1) - c + 1;
+        row0 = pr / p.QG * p.G + pr % p.QG * M::ROWS;
+        rows = min(M::ROWS, p.G - pr % p.QG * M::ROWS);
+    }
+    // every block waits: the end of this kernel is to mean the end of both
+    wait_for_previous();
+    if (n == 0) return;
+    const Part<M::ROWS, D>* parts = static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        __syncthreads();
+        join_row<M>(p, parts, n, r, (int64_t)b * p.Hq + row0 + r);
+    }
 }
 
 template <class M>
@@ -787,7 +863,7 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_early(paged_attn_kernel<M>, dim3(GRID), NT, smem, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_early(paged_join_kernel<M>, dim3(GRID, M::ROWS < p.G ? M::ROWS : p.G), NT, 0,
+    return launch_early(paged_join_kernel<M>, dim3(GRID, p.G < JOIN_Y ? p.G : JOIN_Y), JOIN_NT, 0,
                         stream, p);
 }
 
