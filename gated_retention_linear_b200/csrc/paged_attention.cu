@@ -46,7 +46,8 @@ constexpr int UNIT = 32;               // keys of one unit of work
 constexpr int S = 3;                   // tiles of a warp's ring
 constexpr int HALF = 4096;             // bytes of a tile's keys, and of its values
 constexpr int RING = S * 2 * HALF;
-constexpr int MAXROWS = 32;            // query rows a block works on at a time
+constexpr int MAXROWS_BF16 = 24;       // query rows a block works on at a time: what registers hold
+constexpr int MAXROWS_F32 = 16;
 constexpr int BLOCKS_SM = 2;           // 2 x (4 rings of 24 KB + queries) fill an SM's 227 KB
 constexpr int GRID = 148 * BLOCKS_SM;
 constexpr int JOIN_NT = 128;
@@ -127,6 +128,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // and its 16-byte piece c lies in place c ^ (r & 7), so that reads of one piece of 8 rows, and of
 // one whole row, touch every bank once.
 
+// Where dimension e of row r lies among a warp's sums: 8 lanes of neighbouring dimensions and 4 rows
+// of even number write to 32 banks.
+__device__ __forceinline__ int put_place(int D, int r, int e) {
+    return r * D + (e ^ ((r >> 1 & 3) << 3));
+}
+
 template <int D_, int NQ>
 struct Bf16Math {
     using T = __nv_bfloat16;
@@ -134,7 +141,11 @@ struct Bf16Math {
     static constexpr int QROW = ROWB + 16;           // 16 more bytes: rows begin in other banks
     static constexpr int QBYTES = ROWS * QROW, SCRATCH = 0, NPASS = NQ;
 
-    uint32_t qf[NQ][D / 16][2];
+    // The queries' fragments stay in registers where these suffice; 24 rows of 128 would take 48 on
+    // top of the sums' 96, and are read from shared memory for every 16 keys.
+    static constexpr bool KEEP_Q = NQ * D <= 256;
+
+    uint32_t qf[KEEP_Q ? NQ : 1][D / 16][2];
     float m[NQ][2], l[NQ][2], acc[NQ][D / 16][4];
 
     __device__ static __forceinline__ int q_place(int r, int c) { return r * QROW + c * 16; }
@@ -144,9 +155,12 @@ struct Bf16Math {
         for (int i = 0; i < NQ; ++i) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                const unsigned char* at = qs + (8 * i + lane / 4) * QROW + 32 * k + 4 * (lane & 3);
-                qf[i][k][0] = *reinterpret_cast<const uint32_t*>(at);
-                qf[i][k][1] = *reinterpret_cast<const uint32_t*>(at + 16);
+                if (KEEP_Q) {
+                    const unsigned char* at =
+                        qs + (8 * i + lane / 4) * QROW + 32 * k + 4 * (lane & 3);
+                    qf[i][k][0] = *reinterpret_cast<const uint32_t*>(at);
+                    qf[i][k][1] = *reinterpret_cast<const uint32_t*>(at + 16);
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][k][e] = 0.f;
             }
@@ -157,9 +171,11 @@ struct Bf16Math {
 
     // Bit r of `ok`: key r counts.
     __device__ __forceinline__ void tile(const unsigned char* ks, const unsigned char* vs,
-                                         const unsigned char*, unsigned char*, unsigned ok,
+                                         const unsigned char* qs, unsigned char*, unsigned ok,
                                          float scale, int lane) {
         const uint32_t kb = sm100::smem_u32(ks), vb = sm100::smem_u32(vs);
+        // lanes of a ldmatrix: query row lane % 8, pieces of 8 dimensions lane / 8
+        const uint32_t qb = sm100::smem_u32(qs) + (lane & 7) * QROW + (lane >> 3) * 16;
 #pragma unroll
         for (int j = 0; j < KT; j += 16) {
             float s[NQ][4];
@@ -168,12 +184,25 @@ struct Bf16Math {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t a[4];
+            for (int k = 0; k < D / 16; k += 2) {
+                uint32_t a[2][4];
                 const int r = j + (lane & 15), c = 2 * k + (lane >> 4);
-                ldmatrix4(a, kb + r * ROWB + ((c ^ (r & 7)) << 4));
+                ldmatrix4(a[0], kb + r * ROWB + ((c ^ (r & 7)) << 4));
+                ldmatrix4(a[1], kb + r * ROWB + (((c + 2) ^ (r & 7)) << 4));
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) mma_16x8x16(s[i], a, qf[i][k][0], qf[i][k][1]);
+                for (int i = 0; i < NQ; ++i) {
+                    uint32_t b[4];
+                    if (KEEP_Q) {
+                        b[0] = qf[i][k][0];
+                        b[1] = qf[i][k][1];
+                        b[2] = qf[i][k + 1][0];
+                        b[3] = qf[i][k + 1][1];
+                    } else {
+                        ldmatrix4(b, qb + 8 * i * QROW + 32 * k);
+                    }
+                    mma_16x8x16(s[i], a[0], b[0], b[1]);
+                    mma_16x8x16(s[i], a[1], b[2], b[3]);
+                }
             }
             // s[i]: key lane/4 (0, 1) and lane/4 + 8 (2, 3), queries 8i + 2 (lane & 3) and the next
             const bool ok0 = ok >> (j + lane / 4) & 1, ok1 = ok >> (j + 8 + lane / 4) & 1;
@@ -258,7 +287,7 @@ struct Bf16Math {
             }
     }
 
-    // The sums of 8 rows of values, to rows of D + 4 (so that the lanes' banks differ).
+    // The sums of 8 rows of values, each in put_place's order.
     __device__ __forceinline__ void put(int pass, float* to, int lane) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
@@ -267,7 +296,7 @@ struct Bf16Math {
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        to[(2 * (lane & 3) + (e & 1)) * (D + 4) + 16 * k + lane / 4 + (e >> 1) * 8] =
+                        to[put_place(D, 2 * (lane & 3) + (e & 1), 16 * k + lane / 4 + (e >> 1) * 8)] =
                             acc[i][k][e];
     }
 };
@@ -394,7 +423,7 @@ struct F32Math {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(~0u, x[e], 16);
             if (lane < CPR)
-                *reinterpret_cast<float4*>(to + r * (D + 4) + 4 * lane) =
+                *reinterpret_cast<float4*>(to + put_place(D, r, 4 * lane)) =
                     make_float4(x[0], x[1], x[2], x[3]);
         }
     }
@@ -422,10 +451,10 @@ __device__ __forceinline__ int units_of(const Params& p, int b) {
     return units_between(first, len);
 }
 
-// What ending a pair costs, in units: 0.8 us for each 8 rows, when a block reads 22 KB a us.
+// What ending a pair costs, in units: 1.5 us, and 1.2 for each 8 rows more, when a block reads 22 KB a us.
 template <class M>
 constexpr int end_units() {
-    constexpr int unit_ns = UNIT * 2 * M::ROWB * 1000 / 22000, end_ns = 800 * M::NPASS;
+    constexpr int unit_ns = UNIT * 2 * M::ROWB * 1000 / 22000, end_ns = 300 + 1200 * M::NPASS;
     return (end_ns + unit_ns / 2) / unit_ns < 1 ? 1 : (end_ns + unit_ns / 2) / unit_ns;
 }
 
@@ -689,16 +718,20 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nu;
         Part<M::ROWS, D>* part =
             static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * blockIdx.x + (seg.t0 == 0);
-        // a pass a tile of rows; when the block ends here, nothing is under way, and one pass does
-        constexpr int PR = M::ROWS / M::NPASS;             // rows of a tile
-        const int np = go ? 1 : M::NPASS;
+        // in passes of as many rows as the stage holds; when the block ends here, nothing is under
+        // way, and one pass does
+        constexpr int PR = M::ROWS / M::NPASS;             // rows of a tile of queries
+        constexpr int FIT = 2 * HALF / (PR * D * 4) < M::NPASS ? 2 * HALF / (PR * D * 4) : M::NPASS;
+        static_assert(M::ROWS * D * 4 <= RING && FIT >= 1, "");
+        const int np = go ? FIT : M::NPASS;
         float* mine_put = reinterpret_cast<float*>(
             ring + (go ? (stage == 0 ? S - 1 : stage - 1) * 2 * HALF : 0));
         if (lane == 0) wput[warp] = mine_put;
         math.end(wm[warp], wl[warp], lane);
 #pragma unroll 1
         for (int pass = 0; pass < M::NPASS; pass += np) {
-            for (int i = 0; i < np; ++i) math.put(pass + i, mine_put + i * PR * (D + 4), lane);
+            for (int i = 0; i < np && pass + i < M::NPASS; ++i)
+                math.put(pass + i, mine_put + i * PR * D, lane);
             __syncthreads();
             if (pass == 0 && go) put_q();
             const int row0 = pass * PR, n = min(rows - row0, np * PR);
@@ -712,7 +745,7 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
                     const float f = ex2(wm[w][row] - base);
-                    const float4 x = *reinterpret_cast<const float4*>(wput[w] + r * (D + 4) + e);
+                    const float4 x = *reinterpret_cast<const float4*>(wput[w] + put_place(D, r, e));
                     a[0] += x.x * f;
                     a[1] += x.y * f;
                     a[2] += x.z * f;
@@ -868,22 +901,25 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
 }
 
 // Query rows a block works on at a time: all G heads of a group where they fit, else the fewest
-// equal passes over the keys (each pass reads them again).
+// equal passes over the keys (each pass reads them again), in steps of 8 rows for bf16 and 4 for fp32.
 int rows_of(bool bf16, int G) {
-    if (!bf16) return G <= 4 ? 4 : 8;
-    const int tiles = (G + 7) / 8, passes = (tiles + MAXROWS / 8 - 1) / (MAXROWS / 8);
-    return (tiles + passes - 1) / passes * 8;
+    const int most = bf16 ? MAXROWS_BF16 : MAXROWS_F32, step = bf16 ? 8 : 4;
+    const int passes = (G + most - 1) / most, rows = (G + passes - 1) / passes;
+    return (rows + step - 1) / step * step;
 }
 
 template <int D>
 cudaError_t launch_d(bool bf16, int rows, Params& p, cudaStream_t stream) {
-    if (!bf16)
-        return rows == 4 ? launch<F32Math<D, 4>>(p, stream) : launch<F32Math<D, 8>>(p, stream);
-    switch (rows) {
+    if (bf16) switch (rows) {
         case 8: return launch<Bf16Math<D, 1>>(p, stream);
         case 16: return launch<Bf16Math<D, 2>>(p, stream);
-        case 24: return launch<Bf16Math<D, 3>>(p, stream);
-        default: return launch<Bf16Math<D, 4>>(p, stream);
+        default: return launch<Bf16Math<D, 3>>(p, stream);
+    }
+    switch (rows) {
+        case 4: return launch<F32Math<D, 4>>(p, stream);
+        case 8: return launch<F32Math<D, 8>>(p, stream);
+        case 12: return launch<F32Math<D, 12>>(p, stream);
+        default: return launch<F32Math<D, 16>>(p, stream);
     }
 }
 
