@@ -50,11 +50,17 @@ constexpr int MAXROWS_BF16 = 24;       // query rows a block works on at a time:
 constexpr int MAXROWS_F32 = 16;
 constexpr int BLOCKS_SM = 2;           // 2 x (4 rings of 24 KB + queries) fill an SM's 227 KB
 constexpr int GRID = 148 * BLOCKS_SM;
-constexpr int JOIN_NT = 128;
-constexpr int JOIN_NW = JOIN_NT / 32;
-constexpr int JOIN_Y = 8;              // blocks a pair of the join: 8 x GRID find room at once
+constexpr int JOIN_Y = 8;              // blocks a pair of the join: 8 x GRID are in place at once
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+
+// What the join needs of block c: of the pair whose first part block c holds, and not the rest, the
+// first query row, the rows, and the blocks that hold parts of it (block c's tail slot, then the head
+// slots of the next).  No such pair: no rows.
+struct Header {
+    int32_t head;
+    int16_t rows, parts;
+};
 
 // Parts in the workspace: slot 2c is block c's head (the rest of a pair begun by an earlier
 // block), slot 2c + 1 its tail (a pair that a later block goes on with).
@@ -74,6 +80,7 @@ struct Params {
     void* o;
     float* lse;
     int32_t* status;
+    Header* headers;
     void* parts;
 };
 
@@ -518,7 +525,7 @@ __device__ __forceinline__ void pair_of(int64_t x, int nu, int& pr, int& t) {
 }
 
 struct DealSmem {
-    int64_t scan[JOIN_NW], unit;
+    int64_t scan[NW], unit;
     int b;
 };
 
@@ -529,10 +536,9 @@ __device__ __forceinline__ int64_t dealt_units(const Params& p, int b) {
     return nu ? (int64_t)(nu + end_units<M>()) * (p.pool.H * p.QG) : 0;
 }
 
-// The deal, and the place of the first (`last`: the last) unit of block c: its sequence b, and
-// the first unit of that.  Called by all NT threads; without units for block c, b = -1.
-template <class M, int NT>
-__device__ __forceinline__ Deal deal_of(const Params& p, int c, bool last, DealSmem& sm, int& b,
+// The deal, and the place of the first unit of block c: its sequence b, and the first unit of that.  Called by all NT threads; without units for block c, b = -1.
+template <class M>
+__device__ __forceinline__ Deal deal_of(const Params& p, int c, DealSmem& sm, int& b,
                                         int64_t& unit) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = p.table.S, per = (B + NT - 1) / NT;
@@ -548,7 +554,7 @@ __device__ __forceinline__ Deal deal_of(const Params& p, int c, bool last, DealS
     __syncthreads();
     int64_t U = 0, before = incl - mine;
 #pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
+    for (int w = 0; w < NW; ++w) {
         if (w < warp) before += sm.scan[w];
         U += sm.scan[w];
     }
@@ -556,7 +562,7 @@ __device__ __forceinline__ Deal deal_of(const Params& p, int c, bool last, DealS
     b = -1;
     unit = 0;
     if (c >= U) return d;
-    const int64_t u = last ? d.begin(c + 1) - 1 : d.begin(c);
+    const int64_t u = d.begin(c);
     if (before <= u && u < before + mine) {
         int64_t at = before;
         for (int i = tid * per; i < b1; ++i) {
@@ -592,7 +598,8 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
     let_next_start();
     Segment seg;
     int64_t b_unit;
-    const Deal deal = deal_of<M, NT>(p, blockIdx.x, false, deal_smem, seg.b, b_unit);
+    const Deal deal = deal_of<M>(p, blockIdx.x, deal_smem, seg.b, b_unit);
+    if (tid == 0) p.headers[blockIdx.x] = {0, 0, 0};
     if (seg.b < 0) return;
     const int64_t u0 = deal.begin(blockIdx.x), u1 = deal.begin(blockIdx.x + 1);
     key_range(p, seg.b, seg.first, seg.len);
@@ -718,6 +725,10 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nu;
         Part<M::ROWS, D>* part =
             static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * blockIdx.x + (seg.t0 == 0);
+        if (!whole && seg.t0 == 0 && tid == 0)
+            p.headers[blockIdx.x] = {
+                (int32_t)head0, (int16_t)rows,
+                (int16_t)(deal.block_of(seg.u + seg.nu - 1) - (int)blockIdx.x + 1)};
         // in passes of as many rows as the stage holds; when the block ends here, nothing is under
         // way, and one pass does
         constexpr int PR = M::ROWS / M::NPASS;             // rows of a tile of queries
@@ -772,23 +783,22 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
     }
 }
 
-// Row r of the n parts, to query row `head`: a warp a quarter of the parts, a lane D / 32 dimensions.  All
-// that a row is made of is on its way before any of it is looked at, up to 32 parts.  The block is small
-// so that it finds registers beside the kernel above's, and its deal is done while that one runs.
+// Row r of the n parts, to query row `head`: a warp a quarter of the parts, a lane D / 32 dimensions.
+// All that a row is made of is on its way before any of it is looked at, up to 32 parts.
 template <class M>
 __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M::D>* parts, int n,
                                          int r, int64_t head) {
     using T = typename M::T;
-    constexpr int D = M::D, E = D / 32, UN = 8, PER = (GRID + JOIN_NT - 1) / JOIN_NT;
+    constexpr int D = M::D, E = D / 32, UN = 8, PER = (GRID + NT - 1) / NT;
     __shared__ float w[GRID];                              // the parts' weights
-    __shared__ float sums[JOIN_NW][D], red[2][JOIN_NW];
+    __shared__ float sums[NW][D], red[2][NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // part k: the tail of block c, then the heads of those that follow
     float x[UN][E], m[PER], l[PER];
     auto fetch = [&](int k0) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int k = k0 + i * JOIN_NW;
+            const int k = k0 + i * NW;
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 x[i][e] = k < n ? parts[2 * k + (k == 0)].a[r][lane + 32 * e] : 0.f;
@@ -796,7 +806,7 @@ __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M:
     };
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int k = tid + i * JOIN_NT;
+        const int k = tid + i * NT;
         m[i] = k < n ? parts[2 * k + (k == 0)].m[r] : -INFINITY;
         l[i] = k < n ? parts[2 * k + (k == 0)].l[r] : 0.f;
     }
@@ -808,24 +818,24 @@ __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M:
     if (lane == 0) red[0][warp] = mx;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < JOIN_NW; ++i) mx = fmaxf(mx, red[0][i]);
+    for (int i = 0; i < NW; ++i) mx = fmaxf(mx, red[0][i]);
     const float base = mx == -INFINITY ? 0.f : mx;
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const float f = ex2(m[i] - base);
-        if (tid + i * JOIN_NT < n) w[tid + i * JOIN_NT] = f;
+        if (tid + i * NT < n) w[tid + i * NT] = f;
         z += f * l[i];
     }
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
     if (lane == 0) red[1][warp] = z;
     __syncthreads();
     float a[E] = {};
-    for (int k0 = warp; k0 < n; k0 += JOIN_NW * UN) {
+    for (int k0 = warp; k0 < n; k0 += NW * UN) {
         if (k0 != warp) fetch(k0);
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            const int k = k0 + i * JOIN_NW;
+            const int k = k0 + i * NW;
             const float f = k < n ? w[k] : 0.f;
 #pragma unroll
             for (int e = 0; e < E; ++e) a[e] = fmaf(f, x[i][e], a[e]);
@@ -836,54 +846,38 @@ __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M:
     __syncthreads();
     z = 0.f;
 #pragma unroll
-    for (int i = 0; i < JOIN_NW; ++i) z += red[1][i];
+    for (int i = 0; i < NW; ++i) z += red[1][i];
     if (tid < D) {
         float y = 0.f;
 #pragma unroll
-        for (int i = 0; i < JOIN_NW; ++i) y += sums[i][tid];
+        for (int i = 0; i < NW; ++i) y += sums[i][tid];
         static_cast<T*>(p.o)[head * D + tid] = from_f32<T>(y / z);
     }
     if (p.lse && tid == 0) p.lse[head] = (mx + log2f(z)) * LN2;
 }
 
 // Blocks (c, y) join the parts of the pair that block c of the kernel above began and did not
-// finish, each every JOIN_Y-th row.  Which pair that is follows from the lengths, so this kernel finds
-// it out while the other is still at work.
+// finish, each every JOIN_Y-th row of it.
 template <class M>
-__global__ void __launch_bounds__(JOIN_NT) paged_join_kernel(const Params p) {
+__global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
     using T = typename M::T;
     constexpr int D = M::D;
-    __shared__ DealSmem deal_smem;
     const int tid = threadIdx.x, c = blockIdx.x;
-    // sequences without keys: zeros
+    // sequences without keys: zeros, with nothing to wait for
     for (int b = c; b < p.table.S; b += GRID)
         if (units_of(p, b) == 0)
             for (int i = blockIdx.y; i < p.Hq; i += gridDim.y) {
-                for (int e = tid; e < D; e += JOIN_NT)
+                for (int e = tid; e < D; e += NT)
                     static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * D + e] = from_f32<T>(0.f);
                 if (p.lse && tid == 0) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
             }
-    int b;
-    int64_t b_unit;
-    const Deal deal = deal_of<M, JOIN_NT>(p, c, true, deal_smem, b, b_unit);
-    int n = 0, row0 = 0, rows = 0;                         // parts; their first query row, rows
-    if (b >= 0) {
-        const int64_t u0 = deal.begin(c), u1 = deal.begin(c + 1);
-        const int nu = units_of(p, b);
-        int pr, t;
-        pair_of(u1 - 1 - b_unit, nu + end_units<M>(), pr, t);
-        const int64_t pair0 = u1 - 1 - t;                  // the pair's first unit
-        if (pair0 >= u0 && pair0 + nu > u1) n = deal.block_of(pair0 + nu - 1) - c + 1;
-        row0 = pr / p.QG * p.G + pr % p.QG * M::ROWS;
-        rows = min(M::ROWS, p.G - pr % p.QG * M::ROWS);
-    }
     // every block waits: the end of this kernel is to mean the end of both
     wait_for_previous();
-    if (n == 0) return;
-    const Part<M::ROWS, D>* parts = static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const Header h = p.headers[c];
+    for (int r = blockIdx.y; r < h.rows; r += gridDim.y) {
         __syncthreads();
-        join_row<M>(p, parts, n, r, (int64_t)b * p.Hq + row0 + r);
+        join_row<M>(p, static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c, h.parts, r,
+                    (int64_t)h.head + r);
     }
 }
 
@@ -896,7 +890,7 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_early(paged_attn_kernel<M>, dim3(GRID), NT, smem, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_early(paged_join_kernel<M>, dim3(GRID, p.G < JOIN_Y ? p.G : JOIN_Y), JOIN_NT, 0,
+    return launch_early(paged_join_kernel<M>, dim3(GRID, p.G < JOIN_Y ? p.G : JOIN_Y), NT, 0,
                         stream, p);
 }
 
@@ -926,7 +920,8 @@ cudaError_t launch_d(bool bf16, int rows, Params& p, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_attn_workspace(bool bf16, int Hq, int Hkv, int d) {
-    return (size_t)2 * GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
+    const size_t head = (GRID * sizeof(Header) + 255) / 256 * 256;
+    return head + (size_t)2 * GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
@@ -942,7 +937,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.o = a.o;
     p.lse = a.lse;
     p.status = a.status;
-    p.parts = a.workspace;
+    p.headers = static_cast<Header*>(a.workspace);
+    p.parts = static_cast<unsigned char*>(a.workspace) + (GRID * sizeof(Header) + 255) / 256 * 256;
     const int rows = rows_of(a.bf16, p.G);
     return a.d == 64 ? launch_d<64>(a.bf16, rows, p, stream) : launch_d<128>(a.bf16, rows, p, stream);
 }
