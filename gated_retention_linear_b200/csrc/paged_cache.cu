@@ -27,9 +27,10 @@ constexpr int CL = 8;                  // blocks of a planning cluster (the port
 constexpr int PNT = 1024;
 constexpr int PNW = PNT / 32;
 constexpr int MAXCH = 4 * PNT;         // chunks of ref
-constexpr int GROUP = 4;               // chunks a warp counts at once: 16 loads in flight a lane
+constexpr int GROUP = 4;               // chunks a warp counts at once
 constexpr int GRID = 148 * 4;          // blocks of the kernels that carry a plan out
 constexpr int NT = 256;
+constexpr int APPLY_SM = 6;            // of a resize's: rows wait for lists and counts, not for bandwidth
 constexpr int64_t FORK_ALONE = 1 << 17;   // pairs x table entries that one fork kernel does
 
 // Exclusive sums of x and y over the block's threads, and the totals.  `sums` has 2 PNW entries.
@@ -75,59 +76,85 @@ __device__ __forceinline__ Sums block_scan(int64_t x, int y, int64_t (*sums)[2])
     return r;
 }
 
-// The chunks of ref: chunk c is [c * step, c * step + step), cut off at P.
+// ref, read 16 bytes at a time whatever its alignment: quad j is the entries 4 j - skew and on, where
+// entries before the first and from P on count as taken.  Chunk c is the quads [c * step,
+// c * step + step).
 struct Chunks {
-    int step, n;
+    const int32_t* ref;
+    int P, skew, step, n;
+
+    __device__ __forceinline__ Chunks(const int32_t* r, int pages)
+        : ref(r), P(pages), skew((int)(reinterpret_cast<uintptr_t>(r) >> 2 & 3)) {
+        const int quads = (int)(((int64_t)P + skew + 3) / 4);
+        step = ((quads + MAXCH - 1) / MAXCH + 31) / 32 * 32;
+        n = (quads + step - 1) / step;
+    }
+    __device__ __forceinline__ int entry(int quad) const { return 4 * quad - skew; }
+    __device__ __forceinline__ bool inside(int quad) const {
+        return entry(quad) >= 0 && entry(quad) + 4 <= P;
+    }
+    __device__ __forceinline__ int4 inner_quad(int quad) const {
+        return *reinterpret_cast<const int4*>(ref + entry(quad));
+    }
+    __device__ __forceinline__ int4 quad(int q) const {
+        if (inside(q)) return inner_quad(q);
+        int x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[e] = entry(q) + e >= 0 && entry(q) + e < P ? ref[entry(q) + e] : 1;
+        return make_int4(x[0], x[1], x[2], x[3]);
+    }
 };
 
-__host__ __device__ __forceinline__ Chunks chunks_of(int P) {
-    const int step = ((P + MAXCH - 1) / MAXCH + 127) / 128 * 128;
-    return {step, (P + step - 1) / step};
+__device__ __forceinline__ int free_of(int4 q) {
+    return (q.x == 0) + (q.y == 0) + (q.z == 0) + (q.w == 0);
+}
+
+// The four entries' ranks among the free pages, `before` of which lie before the warp's quads and,
+// afterwards, before the next ones.
+__device__ __forceinline__ int4 ranks_of(int4 q, int& before) {
+    const int lane = threadIdx.x & 31, mine = free_of(q);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    int4 r;
+    r.x = before + incl - mine;
+    r.y = r.x + (q.x == 0);
+    r.z = r.y + (q.y == 0);
+    r.w = r.z + (q.z == 0);
+    before += __shfl_sync(0xffffffffu, incl, 31);
+    return r;
 }
 
 // Counts each chunk's free pages into `count` [MAXCH] of every block of the cluster.  Starts with
 // the second half of a cluster barrier (whoever calls has arrived) and ends with a whole one: what
 // the cluster's blocks read of the inputs beforehand, no block changes before that.
-__device__ __forceinline__ void count_free(const int32_t* ref, int P, int* count) {
+__device__ __forceinline__ void count_free(const Chunks& ch, int* count) {
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = cluster.block_rank() * PNW + (threadIdx.x >> 5);
-    const Chunks ch = chunks_of(P);
     bool begun = false;
     for (int c0 = warp; c0 < ch.n; c0 += CL * PNW * GROUP) {
         int n[GROUP] = {};
-        if ((int64_t)(c0 + (GROUP - 1) * CL * PNW + 1) * ch.step <= P) {
+        const int far = CL * PNW * ch.step, first = c0 * ch.step;
+        if (ch.inside(first) && (int64_t)first + (GROUP - 1) * (int64_t)far + ch.step <= ch.P / 4) {
             // plain loads, so that all of them are on their way before the first is looked at
-            const int32_t* at = ref + (int64_t)c0 * ch.step + lane;
-            const int64_t far = (int64_t)CL * PNW * ch.step;
 #pragma unroll 2
-            for (int i = 0; i < ch.step; i += 128, at += 128) {
-                int x[GROUP][4];
+            for (int i = lane; i < ch.step; i += 32) {
+                int4 x[GROUP];
 #pragma unroll
-                for (int g = 0; g < GROUP; ++g)
+                for (int g = 0; g < GROUP; ++g) x[g] = ch.inner_quad(first + g * far + i);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) x[g][u] = at[g * far + 32 * u];
-#pragma unroll
-                for (int g = 0; g < GROUP; ++g)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) n[g] += x[g][u] == 0;
+                for (int g = 0; g < GROUP; ++g) n[g] += free_of(x[g]);
             }
         } else {
-            for (int i = lane; i < ch.step; i += 128) {
-                int x[GROUP][4];
 #pragma unroll
-                for (int g = 0; g < GROUP; ++g)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int64_t at =
-                            (int64_t)(c0 + g * CL * PNW) * ch.step + i + 32 * u;
-                        x[g][u] = 1;
-                        if (at < P) x[g][u] = ref[at];
-                    }
-#pragma unroll
-                for (int g = 0; g < GROUP; ++g)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) n[g] += x[g][u] == 0;
-            }
+            for (int g = 0; g < GROUP; ++g)
+                if (c0 + g * CL * PNW < ch.n)
+                    for (int i = lane; i < ch.step; i += 32)
+                        n[g] += free_of(ch.quad(first + g * far + i));
         }
         if (!begun) cluster.barrier_wait();      // every block runs: its shared memory can be written
         begun = true;
@@ -144,9 +171,9 @@ __device__ __forceinline__ void count_free(const int32_t* ref, int P, int* count
 
 // Turns the counts into the free pages before each chunk, and returns all of them; the exclusive
 // sum of x over the block's threads goes along.
-__device__ __forceinline__ int rank_free(int P, int* count, int64_t (*sums)[2], int64_t& x) {
+__device__ __forceinline__ int rank_free(const Chunks& ch, int* count, int64_t (*sums)[2],
+                                         int64_t& x) {
     constexpr int PER = MAXCH / PNT;
-    const Chunks ch = chunks_of(P);
     int n[PER], mine = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
@@ -384,9 +411,10 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
         }
         mine += need;
     }
-    count_free(a.ref, a.pool.n_pages, chunk_before);
+    const Chunks ch(a.ref, a.pool.n_pages);
+    count_free(ch, chunk_before);
     int64_t run = mine;
-    const int total = rank_free(a.pool.n_pages, chunk_before, sums, run);
+    const int total = rank_free(ch, chunk_before, sums, run);
     for (int s = s0; s < s1; ++s) {
         run += upto[s];
         upto[s] = (int)(run < INT_MAX ? run : INT_MAX);
@@ -410,36 +438,21 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
             }
         }
     // hand out the free pages of rank < granted
-    const Chunks ch = chunks_of(a.pool.n_pages);
     const int warp = cluster.block_rank() * PNW + (tid >> 5);
     for (int c = warp; c < ch.n && chunk_before[c] < granted; c += CL * PNW) {
         int before = chunk_before[c];
-        const int64_t begin = (int64_t)c * ch.step;
-        for (int i = 0; i < ch.step && before < granted; i += 128) {
-            int x[4], rank[4], l[4], r[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t at = begin + i + 32 * u + lane;
-                x[u] = 1;
-                if (at < a.pool.n_pages) x[u] = a.ref[at];
-            }
+        for (int q0 = c * ch.step; q0 < (c + 1) * ch.step && before < granted; q0 += 32) {
+            const int4 x4 = ch.quad(q0 + lane);
             const int rank0 = before;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const unsigned mask = __ballot_sync(0xffffffffu, x[u] == 0);
-                rank[u] = before + __popc(mask & ((1u << lane) - 1));
-                before += __popc(mask);
-            }
+            const int4 rank4 = ranks_of(x4, before);
             if (before == rank0) continue;
             // the rows of these up to 128 pages, then each page's among them, four searches side by
             // side
             const int row0 = row_of_rank(upto, S, rank0);
             const int row1 = row_of_rank(upto, S, min(before, granted) - 1);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                l[u] = row0;
-                r[u] = row1;
-            }
+            const int x[4] = {x4.x, x4.y, x4.z, x4.w};
+            const int rank[4] = {rank4.x, rank4.y, rank4.z, rank4.w};
+            int l[4] = {row0, row0, row0, row0}, r[4] = {row1, row1, row1, row1};
             for (int n = row1 - row0; n > 0; n >>= 1)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -450,7 +463,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (x[u] != 0 || rank[u] >= granted) continue;
-                const int at = (int)(begin + i + 32 * u + lane), row = r[u];
+                const int at = ch.entry(q0 + lane) + u, row = r[u];
                 a.table.entries[row * a.table.stride + first[row] + rank[u] -
                                 (row ? upto[row - 1] : 0)] = at;
                 a.ref[at] = 1;
@@ -492,9 +505,10 @@ __device__ __forceinline__ void drop_entries(const PagedResizeArgs& a, int32_t* 
     }
 }
 
-__global__ void __launch_bounds__(NT) resize_apply_kernel(const PagedResizeArgs a,
-                                                          const Pieces pc) {
-    __shared__ int from[NT], to[NT], slots[NT], copies;
+__global__ void __launch_bounds__(NT, APPLY_SM) resize_apply_kernel(const PagedResizeArgs a,
+                                                                    const Pieces pc) {
+    constexpr int GRID = APPLY_SM * 148;
+    __shared__ int from[NT], to[NT], slots[NT], in_warp[NT / 32];
     const int tid = threadIdx.x, S = a.table.S, shift = a.pool.page_shift;
     wait_for_previous();
     // a block a row: pages that it drops, its new length
@@ -515,13 +529,21 @@ __global__ void __launch_bounds__(NT) resize_apply_kernel(const PagedResizeArgs 
     int k = blockIdx.x / steps, c = blockIdx.x % steps;   // this block's next: step c of the batch's row k
     const int dk = GRID / steps, dc = GRID % steps;
     for (int s0 = 0; s0 < S; s0 += NT) {
+        // the batch's rows that copy, in order: all blocks have to count them alike
+        const int s = s0 + tid, src = s < S ? a.workspace[s] : -1;
+        const unsigned mask = __ballot_sync(0xffffffffu, src >= 0);
+        __syncthreads();                          // the batch before is done with
+        if ((tid & 31) == 0) in_warp[tid >> 5] = __popc(mask);
         __syncthreads();
-        if (tid == 0) copies = 0;
-        __syncthreads();
-        const int s = s0 + tid;
-        if (s < S && a.workspace[s] >= 0) {
-            const int n0 = a.pos[s], x = atomicAdd(&copies, 1);
-            from[x] = a.workspace[s];
+        int x = __popc(mask & ((1u << (tid & 31)) - 1)), copies = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w < (tid >> 5)) x += in_warp[w];
+            copies += in_warp[w];
+        }
+        if (src >= 0) {
+            const int n0 = a.pos[s];
+            from[x] = src;
             to[x] = a.table.entries[s * a.table.stride + (n0 >> shift)];
             slots[x] = n0 & ((1 << shift) - 1);
         }
@@ -668,42 +690,32 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     let_next_start();
     const int lane = threadIdx.x & 31, P = a.pool.n_pages;
     const CompactPlan plan = compact_plan(a);
-    count_free(a.ref, P, chunk_before);
+    const Chunks ch(a.ref, P);
+    count_free(ch, chunk_before);
     int64_t none = 0;
-    const int L = P - rank_free(P, chunk_before, sums, none);
+    const int L = P - rank_free(ch, chunk_before, sums, none);
     __syncthreads();
     if (cluster.block_rank() == 0 && threadIdx.x == 0) {
         *a.n_live = L;
         plan.counts[0] = L;
         if (L == P) plan.counts[1] = 0;            // no page has the index L
     }
-    const Chunks ch = chunks_of(P);
     for (int c = cluster.block_rank() * PNW + (threadIdx.x >> 5); c < ch.n; c += CL * PNW) {
-        int holes = chunk_before[c];               // free pages before the one at hand
-        const int64_t begin = (int64_t)c * ch.step;
-        for (int i = 0; i < ch.step; i += 128) {
-            int x[4];
+        int before = chunk_before[c];
+        for (int q0 = c * ch.step; q0 < (c + 1) * ch.step; q0 += 32) {
+            const int4 x4 = ch.quad(q0 + lane), h4 = ranks_of(x4, before);
+            const int x[4] = {x4.x, x4.y, x4.z, x4.w}, h[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int64_t at = begin + i + 32 * u + lane;
-                x[u] = 1;
-                if (at < P) x[u] = a.ref[at];
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t at = begin + i + 32 * u + lane;
-                const unsigned mask = __ballot_sync(0xffffffffu, x[u] == 0);
-                const int h = holes + __popc(mask & ((1u << lane) - 1));
-                if (at < P) {
-                    if (at == L) plan.counts[1] = h;   // holes below L = pages in use past it
-                    if (at < L) {
-                        if (x[u] == 0) plan.holes[h] = (int)at;
-                    } else {
-                        plan.rank[at] = x[u] == 0 ? -1 : (int)at - h;
-                        if (x[u] != 0) plan.used[at - h] = (int)at;
-                    }
+                const int at = ch.entry(q0 + lane) + u;
+                if (at < 0 || at >= P) continue;
+                if (at == L) plan.counts[1] = h[u];    // holes below L = pages in use past it
+                if (at < L) {
+                    if (x[u] == 0) plan.holes[h[u]] = at;
+                } else {
+                    plan.rank[at] = x[u] == 0 ? -1 : at - h[u];
+                    if (x[u] != 0) plan.used[at - h[u]] = at;
                 }
-                holes += __popc(mask);
             }
         }
     }
@@ -775,7 +787,7 @@ cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_early(resize_plan_kernel, dim3(CL), PNT, smem, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_early(resize_apply_kernel, dim3(GRID), NT, 0, stream, a, Pieces(a.pool));
+    return launch_early(resize_apply_kernel, dim3(APPLY_SM * 148), NT, 0, stream, a, Pieces(a.pool));
 }
 
 cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {

@@ -1,0 +1,274 @@
+"""The paged key-value cache at the sizes where its kernels change their ways: many rows that copy at
+once, pages of several copy steps, page counts at every alignment, forks with counts added once or
+one by one, every number of query rows a pass, sequences in one part and in hundreds, and calls
+queued without a wait in between."""
+import numpy as np
+import pytest
+import torch
+
+from paged_model import Cache
+from test_paged_gpu import BF16, F32, Dev, check, filled, i32, lib, queries, resize
+
+pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------------------------- attention
+
+
+@pytest.mark.parametrize("dtype,d,G", [
+    (BF16, 64, 1), (BF16, 64, 8), (BF16, 64, 15), (BF16, 64, 16), (BF16, 64, 17), (BF16, 64, 24),
+    (BF16, 128, 8), (BF16, 128, 12), (BF16, 128, 17), (BF16, 128, 24), (BF16, 128, 25),
+    (BF16, 128, 32), (BF16, 128, 48),
+    (F32, 64, 4), (F32, 64, 5), (F32, 64, 8), (F32, 64, 12), (F32, 64, 16), (F32, 64, 17),
+    (F32, 128, 4), (F32, 128, 7), (F32, 128, 9), (F32, 128, 13), (F32, 128, 16), (F32, 128, 24),
+])
+def test_attention_group_sizes(dtype, d, G):
+    """Every number of rows a block works on, as many as it holds, one more, and several passes; two
+    kv heads, so that groups lie side by side; sequences that end in one block and ones that do not."""
+    lens = [1, 700, 33, 0, 95, 2500]
+    c = filled(lens, 16, 2, d, dtype, seed=G + d)
+    dev, q = Dev(c), queries(len(lens), 2 * G, d, dtype, seed=G)
+    o, lse = dev.decode(q)
+    check(c, q, o, lse)
+    o, lse = dev.decode(q, window=90)
+    check(c, q, o, lse, 90)
+    assert int(dev.status) == 0
+
+
+@pytest.mark.parametrize("dtype,d,G,n", [
+    (BF16, 128, 1, 9473), (BF16, 128, 20, 9500), (BF16, 64, 3, 20001), (F32, 64, 2, 9472),
+    (F32, 128, 16, 9600), (BF16, 128, 3, 31), (BF16, 128, 3, 33), (BF16, 64, 9, 9471),
+])
+def test_attention_one_pair_over_all_blocks(dtype, d, G, n):
+    """One sequence with one kv head: up to 296 parts (and, with few keys, blocks without any)."""
+    c = filled([n], 32, 1, d, dtype, seed=n)
+    dev, q = Dev(c), queries(1, G, d, dtype, seed=n)
+    o, lse = dev.decode(q)
+    check(c, q, o, lse)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_attention_borders(seed):
+    """Lengths around the borders of tiles, units and blocks, many pairs a block and pairs that end
+    with a block, in batches of every density."""
+    rng = np.random.default_rng(seed)
+    B = [1, 3, 20, 70, 130, 300][seed]
+    near = np.array([1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 0, 512])
+    lens = rng.choice(near, B) + (rng.random(B) < 0.1) * rng.integers(0, 900, B)
+    H, G, d = [(8, 3, 128), (3, 8, 64), (4, 1, 128), (1, 5, 64), (2, 12, 128), (1, 2, 64)][seed]
+    dtype = F32 if seed in (2, 5) else BF16
+    c = filled(lens.tolist(), [16, 8, 32, 1, 16, 64][seed], H, d, dtype, seed=40 + seed)
+    dev, q = Dev(c, seed % 2 == 1), queries(B, H * G, d, dtype, seed)
+    o, lse = dev.decode(q)
+    check(c, q, o, lse)
+
+
+# -------------------------------------------------------------------------------- upkeep
+
+
+@pytest.mark.parametrize("dtype,S,beam,H,d,page,hm", [
+    (BF16, 256, 4, 8, 128, 16, False), (BF16, 700, 5, 3, 64, 16, True), (F32, 300, 2, 2, 128, 32, True),
+    (F32, 520, 40, 1, 16, 64, False), (BF16, 40, 3, 5, 48, 128, False),
+])
+def test_resize_many_copies(dtype, S, beam, H, d, page, hm):
+    """Hundreds of rows leave shared pages of several copy steps in one call, beside rows that do
+    not grow; and once more, when the copies are nobody else's."""
+    rng = np.random.default_rng(S)
+    lens = np.repeat(rng.integers(1, 3 * page, -(-S // beam)), beam)[:S]
+    lens[rng.random(S) < 0.1] = 0                     # idle rows among them
+    first = np.arange(S) // beam * beam
+    lens[first[lens[first] == 0]] = 0
+    lens = np.where(lens[first] == 0, 0, lens)
+    parents = np.where(first == np.arange(S), lens, 0)
+    c = filled(parents.tolist(), page, H, d, dtype, seed=S, spare=3 * S)
+    c.table = np.concatenate([c.table, np.full((S, 2), -1, np.int32)], 1)
+    c.W += 2
+    for s in np.flatnonzero((first != np.arange(S)) & (lens > 0)):
+        n = c.pages(lens[s])
+        c.table[s], c.lens[s] = c.table[first[s]], lens[s]
+        c.ref[c.table[s, :n]] += 1
+    dev = Dev(c, hm)
+    delta = np.where(rng.random(S) < 0.8, rng.integers(0, page + 2, S), -rng.integers(1, page, S))
+    resize(dev, c, delta)
+    resize(dev, c, np.ones(S, int))
+
+
+@pytest.mark.parametrize("off", range(4))
+@pytest.mark.parametrize("P", [1, 2, 3, 5, 127, 4095, 16387, 600000])
+def test_pool_alignments(off, P):
+    """ref at each place within 16 bytes, pools whose last pages do not fill a load."""
+    rng = np.random.default_rng(P + off)
+    S = 4
+    c = Cache(S=S, W=min(P, 3000) + 1, P=P, page=1, H=1, d=8, dtype=BF16)
+    taken = rng.random(P) < 0.3
+    c.ref[taken] = 1                                  # held by nobody in the table
+    dev = Dev(c)
+    wide = torch.full((P + 8,), 0, dtype=torch.int32, device="cuda")      # zeros around: free, if read
+    dev.ref = wide[off:off + P]
+    dev.ref.copy_(i32(c.ref))
+    free = min(int((~taken).sum()), 3000)             # of it, what a row's table holds
+    resize(dev, c, [free // 7, 0, free // 5, free // 3])
+    resize(dev, c, [-(free // 9), free // 11, 0, -free])
+    n = lib().gret_paged_compact(dev.lens, dev.table, dev.ref, dev.k, dev.v, status=dev.status)
+    assert int(n) == c.compact()
+    dev.same_as(c)
+    assert int(wide[:off].sum()) == 0 and int(wide[off + P:].sum()) == 0 and int(dev.status) == 0
+
+
+@pytest.mark.parametrize("parents,children,pages", [
+    (1, 1, 5000), (2, 3, 9000), (3, 40, 4097), (2, 1300, 120), (5, 60, 2000), (4, 64, 76),
+])
+def test_fork_kinds(parents, children, pages):
+    """Few long rows, many short ones, and pairs that are refused among those that share a source."""
+    rng = np.random.default_rng(pages)
+    S = parents + children + 3
+    c = Cache(S=S, W=pages, P=2 * parents * pages, page=4, H=1, d=8, dtype=F32)
+    ids = rng.permutation(len(c.ref))
+    for s in range(parents):
+        c.lens[s] = rng.integers(pages * 2, pages * 4 + 1)
+        n = c.pages(c.lens[s])
+        c.table[s, :n] = ids[s * pages:s * pages + n]
+        if s:                                         # a prefix shared by all parents
+            c.table[s, :n // 3] = c.table[0, :n // 3] if n // 3 <= c.pages(c.lens[0]) else ids[:n // 3]
+    np.add.at(c.ref, c.table[c.table >= 0], 1)
+    c.lens[S - 1] = 1                                 # not empty, and holds a page of its own
+    c.table[S - 1, 0] = ids[-1]
+    c.ref[ids[-1]] += 1
+    dev = Dev(c)
+    src = rng.integers(0, parents, children + 4)
+    dst = np.concatenate([parents + rng.permutation(children), [S - 1, parents, S, 0 if parents > 2 else -1]])
+    order = rng.permutation(children + 4)
+    src, dst = src[order], dst[order]
+    seen, ok = set(), []
+    for i, (s, t) in enumerate(zip(src, dst)):
+        ok.append(0 <= t < S and c.lens[t] == 0 and t not in seen and s not in dst)
+        seen.add(t)
+    lib().gret_paged_fork(i32(src), i32(dst), dev.lens, dev.table, dev.ref, 4, status=dev.status)
+    for s, t in zip(src[ok], dst[ok]):
+        n = c.pages(c.lens[s])
+        c.table[t, :n], c.lens[t] = c.table[s, :n], c.lens[s]
+        c.ref[c.table[s, :n]] += 1
+    assert not all(ok) and any(ok)
+    dev.same_as(c)
+    assert lib().gret_paged_status(dev.status) == lib().GRET_PAGED_BAD_ROW
+
+
+@pytest.mark.parametrize("dtype,H,d,T", [
+    (BF16, 8, 128, 9471), (BF16, 8, 128, 9473), (F32, 3, 24, 30001), (BF16, 1, 8, 80000),
+    (F32, 2, 64, 1),
+])
+def test_append_token_counts(dtype, H, d, T):
+    """One token a warp and several, with the last warp's not all there; rows cut at random, empty
+    ones among them, from inputs that are parts of wider ones."""
+    rng = np.random.default_rng(T)
+    S, page = 50, 16
+    cu = np.sort(np.concatenate([[3 % T, T], rng.integers(3 % T, T + 1, S - 1)]))
+    new = np.diff(cu)
+    start = rng.integers(0, 40, S)
+    c = Cache(S, int((start + new).max()) // page + 2, int(((start + new) // page + 1).sum()), page, H,
+              d, dtype)
+    at = 0
+    for s in range(S):
+        n = c.pages(start[s] + new[s])
+        c.table[s, :n] = np.arange(at, at + n)
+        at += n
+    dev = Dev(c)
+    kv = torch.randn((T, 2, H, d)).to(dtype)
+    pos = np.where(rng.random(S) < 0.1, -1, start)
+    for s in range(S):
+        if pos[s] >= 0:
+            t = pos[s] + np.arange(new[s])
+            pg, sl = torch.from_numpy(c.table[s, t // page]).long(), torch.from_numpy(t % page)
+            c.k[pg, sl], c.v[pg, sl] = kv[cu[s]:cu[s + 1], 0], kv[cu[s]:cu[s + 1], 1]
+    both = kv.cuda()
+    lib().gret_paged_append(both[:, 0], both[:, 1], i32(pos), dev.table, dev.k, dev.v,
+                            cu_seqlens=i32(cu), status=dev.status)
+    dev.same_as(c)
+    assert int(dev.status) == 0
+
+
+# -------------------------------------------------------------------------------- together
+
+
+def test_queued_calls():
+    """Sixty steps of resize, append, fork, compact and attention queued behind one another, each
+    call's outputs the next one's inputs, with nothing waited for before the end; on the current
+    stream and on one that is given."""
+    G = lib()
+    S, H, d, page = 40, 2, 64, 8
+    for side in (None, torch.cuda.Stream()):
+        rng = np.random.default_rng(50)
+        c = filled([50, 0, 9] + [0] * (S - 3), page, H, d, BF16, seed=50, spare=400)
+        c.table = np.concatenate([c.table, np.full((S, 12), -1, np.int32)], 1)
+        c.W += 12
+        dev = Dev(c)
+        steps = []
+        for step in range(60):
+            delta = np.where(c.lens > 0, 1, 0)
+            if step % 5 == 4:
+                delta[rng.integers(0, S, 3)] = -2 ** 31
+            if step % 5 == 1:
+                delta[0] = 1                          # a new sequence, if the row is idle
+            pos, refused = c.resize(delta)
+            assert refused == []
+            k, v = (torch.randn((S, H, d)).to(BF16) for _ in range(2))
+            for s in np.flatnonzero(pos >= 0):
+                c.append(s, pos[s], k[s:s + 1], v[s:s + 1])
+            src, dst = rng.integers(0, S, 4), rng.integers(0, S, 4)
+            c.fork(src.tolist(), dst.tolist())
+            if step % 9 == 8:
+                c.compact()
+            steps.append((i32(delta), k.cuda(), v.cuda(), i32(src), i32(dst), step % 9 == 8))
+        q = queries(S, 6, d, BF16, 50)
+        torch.cuda.synchronize()
+        outs = []
+        for delta, k, v, src, dst, compact in steps:
+            pos = G.gret_paged_resize(delta, dev.lens, dev.table, dev.ref, dev.k, dev.v, stream=side)
+            G.gret_paged_append(k, v, pos, dev.table, dev.k, dev.v, stream=side)
+            if side is None:
+                del pos                               # its memory may go to the next call
+            G.gret_paged_fork(src, dst, dev.lens, dev.table, dev.ref, page, stream=side)
+            if compact:
+                G.gret_paged_compact(dev.lens, dev.table, dev.ref, dev.k, dev.v, stream=side)
+            outs.append(G.gret_paged_attention_decode(q, dev.lens, dev.table, dev.k, dev.v, lse=True,
+                                                      stream=side))
+        torch.cuda.synchronize()
+        dev.same_as(c)
+        check(c, q, *outs[-1])
+
+
+def test_binding_scope():
+    """What the binding refuses on a GPU, and that a stream given does not stay current."""
+    G = lib()
+    c = filled([20], 16, 1, 64, BF16, seed=60)
+    dev, q = Dev(c), queries(1, 2, 64, BF16, 60)
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    o, none = G.gret_paged_attention_decode(q, dev.lens, dev.table, dev.k, dev.v, stream=side)
+    assert none is None and torch.cuda.current_stream() == here
+    side.synchronize()
+    lse = torch.zeros((1, 2), device="cuda")
+    dec = G.gret_paged_attention_decode
+    for error, f in [
+        (TypeError, lambda: dec(q, dev.lens, dev.table, dev.k, dev.v, stream=3)),
+        (TypeError, lambda: dec(q, None, dev.table, dev.k, dev.v)),
+        (TypeError, lambda: dec(q, dev.lens, dev.table, dev.k, dev.v, window=1.5)),
+        (ValueError, lambda: dec(q, dev.lens, dev.table, dev.k, dev.v, window=2 ** 31)),
+        (ValueError, lambda: dec(q, dev.lens.repeat(2), dev.table, dev.k, dev.v)),
+        (ValueError, lambda: dec(q, dev.lens, dev.table, dev.k, dev.v, lse=lse[0])),
+        (ValueError, lambda: dec(q, dev.lens, dev.table, dev.k, dev.v, lse=lse.cpu())),
+        (ValueError, lambda: dec(q, dev.lens, dev.table, dev.k, dev.v, status=dev.ref[:2])),
+        (ValueError, lambda: dec(q.transpose(0, 1), dev.lens.repeat(2), dev.table, dev.k, dev.v)),
+        (ValueError, lambda: G.gret_paged_resize(dev.lens.long(), dev.lens, dev.table, dev.ref, dev.k,
+                                                 dev.v)),
+        (ValueError, lambda: G.gret_paged_fork(dev.lens, dev.lens, dev.lens, dev.table, dev.ref, 2 ** 40)),
+        (G.GretError, lambda: G.gret_paged_fork(dev.lens, dev.lens, dev.lens, dev.table, dev.ref, 24)),
+        (G.GretError, lambda: dec(q, dev.lens, dev.table, dev.k, dev.v, scale=float("inf"))),
+    ]:
+        with pytest.raises(error):
+            f()
+    dev.same_as(c)
+    o2, got = dec(q, dev.lens, dev.table, dev.k, dev.v, scale=1, lse=lse)   # an integer scale
+    assert got is lse
+    check(c, q, o2, lse, scale=1)
+    check(c, q, o, G.gret_paged_attention_decode(q, dev.lens, dev.table, dev.k, dev.v, lse=True)[1])
