@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gret.h"
 
 namespace gret {
@@ -127,6 +129,22 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size
     cfg.attrs = &early;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// Dynamic shared memory of `bytes`, at most `most`, for a kernel: up to 24 KB beside its own arrays need
+// no leave; for more it is asked once on each of the first 64 devices.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes, int most) {
+    static std::atomic<uint64_t> given{0};
+    if (bytes <= 24 * 1024) return cudaSuccess;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+    if (given.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess) given.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 __device__ __forceinline__ void wait_for_previous() {

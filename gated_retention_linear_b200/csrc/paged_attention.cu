@@ -885,8 +885,7 @@ template <class M>
 cudaError_t launch(Params& p, cudaStream_t stream) {
     constexpr int smem = NW * (RING + M::SCRATCH) + M::QBYTES;
     p.QG = (p.G + M::ROWS - 1) / M::ROWS;
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<M>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<paged_attn_kernel<M>>(smem, smem);
     if (e != cudaSuccess) return e;
     e = launch_early(paged_attn_kernel<M>, dim3(GRID), NT, smem, stream, p);
     if (e != cudaSuccess) return e;

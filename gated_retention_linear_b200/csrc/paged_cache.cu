@@ -239,13 +239,6 @@ __device__ __forceinline__ void copy_pieces(const PagedPool& p, const Pieces& pc
     }
 }
 
-// Up to 24 KB beside a kernel's own arrays need no leave.
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    if (bytes <= 24 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 // ---------------------------------------------------------------------------------------------
 // append: a copy of every token's row of heads to its slot.  Bound by HBM, each byte read and
 // written once; with few tokens by the chain row -> position -> page -> copy, so a warp's lanes
@@ -329,6 +322,8 @@ __global__ void __launch_bounds__(NT) append_kernel(const PagedAppendArgs a, con
 // ---------------------------------------------------------------------------------------------
 // resize: a plan by one cluster (who gets which page), then the whole GPU carries it out.
 
+constexpr int ROWS_U = 4;              // rows that a planning thread looks at at once
+
 // A row's change, from its length before the call.
 struct Change {
     int64_t n0, n1;
@@ -379,37 +374,49 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
     const int per = (S + PNT - 1) / PNT;
     const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
     int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) {
-        const Change c = change_of(a, s);
-        int need = 0, src = -1;
-        bool grown = false;
-        first[s] = 0;
-        if (c.bad) {
-            if (lead) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
-        } else if (c.n1 > c.n0) {
-            if (c.n1 > (int64_t)a.table.max_pages << shift) {
-                if (lead) paged_flag(a.status, GRET_PAGED_TABLE_FULL);
-            } else {
-                const int c0 = pages_of(c.n0, shift), c1 = pages_of(c.n1, shift);
-                if (c.n0 & ((1 << shift) - 1)) {
-                    const int id = a.table.entries[s * a.table.stride + c0 - 1];
-                    if ((unsigned)id >= (unsigned)a.pool.n_pages) {
-                        if (lead) paged_flag(a.status, GRET_PAGED_BAD_PAGE);
-                    } else if (a.ref[id] > 1) {
-                        src = id;
-                    }
+    for (int sb = s0; sb < s1; sb += ROWS_U) {
+        // length, last page, its count: three loads one after another, of ROWS_U rows side by side
+        Change c[ROWS_U];
+        int id[ROWS_U], count[ROWS_U];
+        bool fits[ROWS_U];
+#pragma unroll
+        for (int u = 0; u < ROWS_U; ++u) {
+            c[u] = {0, 0, false};
+            if (sb + u < s1) c[u] = change_of(a, sb + u);
+        }
+#pragma unroll
+        for (int u = 0; u < ROWS_U; ++u) {
+            fits[u] = !c[u].bad && c[u].n1 > c[u].n0 &&
+                      c[u].n1 <= (int64_t)a.table.max_pages << shift;
+            id[u] = -1;
+            if (fits[u] && (c[u].n0 & ((1 << shift) - 1))) {
+                id[u] = a.table.entries[(sb + u) * a.table.stride + (c[u].n0 >> shift)];
+                if ((unsigned)id[u] >= (unsigned)a.pool.n_pages) {
+                    if (lead) paged_flag(a.status, GRET_PAGED_BAD_PAGE);
+                    id[u] = -1;
                 }
-                need = c1 - c0 + (src >= 0);
-                first[s] = c0 - (src >= 0);
-                grown = true;
             }
         }
-        upto[s] = need;
-        if (lead) {
-            a.workspace[s] = src;
-            a.pos[s] = grown ? (int)c.n0 : -1;
+#pragma unroll
+        for (int u = 0; u < ROWS_U; ++u) count[u] = id[u] >= 0 ? a.ref[id[u]] : 0;
+#pragma unroll
+        for (int u = 0; u < ROWS_U; ++u) {
+            const int s = sb + u;
+            if (s >= s1) break;
+            if (lead && c[u].bad) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
+            if (lead && !c[u].bad && c[u].n1 > c[u].n0 && !fits[u])
+                paged_flag(a.status, GRET_PAGED_TABLE_FULL);
+            const int c0 = pages_of(c[u].n0, shift), c1 = pages_of(c[u].n1, shift);
+            const bool copies = count[u] > 1;
+            const int need = fits[u] ? c1 - c0 + copies : 0;
+            upto[s] = need;
+            first[s] = fits[u] ? c0 - copies : 0;
+            if (lead) {
+                a.workspace[s] = copies ? id[u] : -1;
+                a.pos[s] = fits[u] ? (int)c[u].n0 : -1;
+            }
+            mine += need;
         }
-        mine += need;
     }
     const Chunks ch(a.ref, a.pool.n_pages);
     count_free(ch, chunk_before);
@@ -783,7 +790,7 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)a.table.S * 2 * sizeof(int);
-    cudaError_t e = allow_smem(resize_plan_kernel, smem);
+    cudaError_t e = allow_smem<resize_plan_kernel>(smem, PAGED_MAX_SEQS * 2 * (int)sizeof(int));
     if (e != cudaSuccess) return e;
     e = launch_early(resize_plan_kernel, dim3(CL), PNT, smem, stream, a);
     if (e != cudaSuccess) return e;
@@ -797,12 +804,12 @@ cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
     // Alone a block a pair, rows of up to 4 steps of a block, and no more atomics than take a
     // microsecond or two on few addresses.
     if (a.table.max_pages <= 4096 && (int64_t)a.n * a.table.max_pages <= FORK_ALONE) {
-        e = allow_smem(fork_kernel<false>, smem);
+        e = allow_smem<fork_kernel<false>>(smem, PAGED_MAX_SEQS * (int)sizeof(int));
         if (e != cudaSuccess) return e;
         return launch_early(fork_kernel<false>, dim3(x), NT, smem, stream, a);
     }
-    e = allow_smem(fork_kernel<true>, smem);
-    if (e == cudaSuccess) e = allow_smem(fork_lengths_kernel, smem);
+    e = allow_smem<fork_kernel<true>>(smem, PAGED_MAX_SEQS * (int)sizeof(int));
+    if (e == cudaSuccess) e = allow_smem<fork_lengths_kernel>(smem, PAGED_MAX_SEQS * (int)sizeof(int));
     if (e != cudaSuccess) return e;
     // a block a pair; with few pairs a row is cut up, in pieces of 1024 entries at least
     int y = 2 * GRID / x, most = (a.table.max_pages + 1023) / 1024;
