@@ -355,7 +355,7 @@ __device__ __forceinline__ int row_of_rank(const int* upto, int S, int rank) {
 
 // Leaves pos, the new pages' ref and table entries, and in workspace[s] the page that row s is to
 // copy its last, partly filled one from (-1: none).
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT, 1)
     resize_plan_kernel(const PagedResizeArgs a) {
     extern __shared__ int rows_smem[];
     __shared__ int64_t sums[PNW][2];
@@ -687,7 +687,7 @@ __host__ __device__ __forceinline__ CompactPlan compact_plan(const PagedCompactA
     return {a.workspace, a.workspace + 4, a.workspace + 4 + P, a.workspace + 4 + 2 * P};
 }
 
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT)
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT, 1)
     compact_plan_kernel(const PagedCompactArgs a) {
     __shared__ int64_t sums[PNW][2];
     __shared__ int chunk_before[MAXCH];
