@@ -32,6 +32,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -43,6 +45,8 @@ namespace {
 constexpr int NT = 128;
 constexpr int NW = NT / 32;
 constexpr int UNIT = 32;               // keys of one unit of work
+constexpr int SHORT_TILES = 8;         // pairs of up to so many are worked on by single warps,
+constexpr int MIN_SHORT = 592;         // where there are at least so many of them
 constexpr int S = 3;                   // tiles of a warp's ring
 constexpr int HALF = 4096;             // bytes of a tile's keys, and of its values
 constexpr int RING = S * 2 * HALF;
@@ -147,6 +151,7 @@ struct Bf16Math {
     static constexpr int D = D_, ROWS = 8 * NQ, ROWB = D * 2, KT = HALF / ROWB;
     static constexpr int QROW = ROWB + 16;           // 16 more bytes: rows begin in other banks
     static constexpr int QBYTES = ROWS * QROW, SCRATCH = 0, NPASS = NQ;
+    static constexpr bool BY_WARPS = false, SPARE = ROWS * D <= 1536;   // see ByWarps
 
     // The queries' fragments stay in registers where these suffice; 24 rows of 128 would take 48 on
     // top of the sums' 96, and are read from shared memory for every 16 keys.
@@ -157,7 +162,7 @@ struct Bf16Math {
 
     __device__ static __forceinline__ int q_place(int r, int c) { return r * QROW + c * 16; }
 
-    __device__ __forceinline__ void begin(const unsigned char* qs, unsigned char*, int lane) {
+    __device__ __forceinline__ void begin(const unsigned char* qs, int lane) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
 #pragma unroll
@@ -316,6 +321,7 @@ struct F32Math {
     // a query row in parts of 32 dimensions, 16 bytes between them: the parts begin in other banks
     static constexpr int QROW = D / 32 * 144;
     static constexpr int QBYTES = R * QROW, SCRATCH = KT * R * 4, NPASS = 1;
+    static constexpr bool BY_WARPS = false, SPARE = R * D <= 1024;
 
     float m[R], l[R];
     float2 acc[R][2];            // dimensions 4 (lane % CPR) and on
@@ -324,7 +330,7 @@ struct F32Math {
         return r * QROW + c / 8 * 144 + c % 8 * 16;
     }
 
-    __device__ __forceinline__ void begin(const unsigned char*, unsigned char*, int) {
+    __device__ __forceinline__ void begin(const unsigned char*, int) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m[r] = -INFINITY;
@@ -436,6 +442,18 @@ struct F32Math {
     }
 };
 
+// The same with short pairs worked on by single warps.  A block takes 1.5 us and more to end a pair, and
+// one warp little longer for a short one altogether, while the block's others do as much: 187 x 16 pairs
+// of 2 keys 32 -> 16 us, 192 x 16 of 70 keys of 64 dimensions 32 -> 22.  A kernel of its own, for
+// batches that may have enough such pairs: others would be 3 to 6 % slower for the code that they have
+// no use for.  Not where the rows' sums leave no registers to spare (SPARE): there the kernel would be
+// 9 % slower on batches that are long after all.
+template <class M>
+struct ByWarps : M {
+    static constexpr bool BY_WARPS = true;
+    static_assert(M::QBYTES <= 2 * HALF, "a stage of the ring holds the queries");
+};
+
 // Keys [first, len) of sequence b.
 __device__ __forceinline__ void key_range(const Params& p, int b, uint32_t& first, uint32_t& len) {
     const int64_t cap = (int64_t)p.table.max_pages << p.pool.page_shift;
@@ -465,20 +483,52 @@ constexpr int end_units() {
     return (end_ns + unit_ns / 2) / unit_ns < 1 ? 1 : (end_ns + unit_ns / 2) / unit_ns;
 }
 
-// A stretch of one pair's units that a block works on: units [t0, t1) of the nu that hold keys;
-// `last` units for the pair's end follow those in the count.
-struct Segment {
-    int64_t u;                   // of the whole batch's units, the one t0 stands for
-    uint32_t first, len;
-    int b, pr, nu, t0, t1, last;
+// The sequences that a walk over the batch stops at.
+enum Kind : int { ANY, LONG, SHORT };
 
+template <class M>
+__device__ __forceinline__ bool is_short(uint32_t first, uint32_t len) {
+    return M::BY_WARPS && len - first <= SHORT_TILES * M::KT;
+}
+
+// A stretch of one pair's units that a block works on: units [t0, t1) of the nu that hold keys;
+// end_units() units for the pair's end follow those in the count.
+template <class M>
+struct Segment {
+    static constexpr int LAST = end_units<M>();
+
+    int64_t u;                   // of all units of this kind, the one t0 stands for
+    uint32_t first, len;
+    int b, pr, nu, t0, t1;
+
+    // At unit u, in sequence b_, whose units begin at b_unit, of those dealt up to u1; false if there
+    // are no keys in [u, u1).
+    __device__ __forceinline__ bool start(const Params& p, Kind kind, int b_, int64_t b_unit,
+                                          int64_t u_, int64_t u1) {
+        b = b_;
+        u = u_;
+        key_range(p, b, first, len);
+        nu = units_between(first, len);
+        const int64_t x = u - b_unit;             // = pr (nu + LAST) + t0
+        if (x <= INT_MAX) {                       // a fifth of the time of a division in 64 bits
+            pr = (int)x / (nu + LAST);
+            t0 = (int)x % (nu + LAST);
+        } else {
+            pr = (int)(x / (nu + LAST));
+            t0 = (int)(x % (nu + LAST));
+        }
+        t1 = (int)min((int64_t)nu, t0 + (u1 - u));
+        // short pairs belong whole to the warp that their first unit is dealt to; a range may also
+        // begin among the units of an end
+        return t0 >= (kind == SHORT ? 1 : nu) ? next(p, kind, u1) : kind != SHORT || (t1 = nu, true);
+    }
     __device__ __forceinline__ uint32_t key0() const { return first + (uint32_t)t0 * UNIT; }
     __device__ __forceinline__ uint32_t key1() const {
         return t1 == nu ? len : first + (uint32_t)t1 * UNIT;
     }
-    // To the next one of a block whose units end before u1.
-    __device__ __forceinline__ bool next(const Params& p, int64_t u1) {
-        u += nu + last - t0;
+    // To the next one of a range that ends before u1.
+    __device__ __forceinline__ bool next(const Params& p, Kind kind, int64_t u1) {
+        u += nu + LAST - t0;
         if (u >= u1) return false;
         t0 = 0;                  // only a block's last segment ends inside its pair
         if (++pr == p.pool.H * p.QG) {
@@ -486,182 +536,206 @@ struct Segment {
             do {
                 if (++b == p.table.S) return false;
                 key_range(p, b, first, len);
-            } while (len == first);
+            } while (len == first || (kind != ANY && (kind == SHORT) != is_short<M>(first, len)));
             nu = units_between(first, len);
         }
-        t1 = (int)min((int64_t)nu, u1 - u);
+        t1 = kind == SHORT ? nu : (int)min((int64_t)nu, u1 - u);
         return true;
+    }
+    // Its queries: the first of them, and how many.
+    __device__ __forceinline__ int64_t head(const Params& p) const {
+        return (int64_t)b * p.Hq + pr / p.QG * p.G + pr % p.QG * M::ROWS;
+    }
+    __device__ __forceinline__ int rows(const Params& p) const {
+        return min(M::ROWS, p.G - pr % p.QG * M::ROWS);
     }
 };
 
-// How the batch's U units are dealt: block c has units [begin(c), begin(c + 1)), each of the first
-// `more` blocks one more than the others' `each`.  With fewer units than blocks, the first U blocks
-// take one each: a pair's parts lie in consecutive blocks.  A pair counts for more units than its
-// keys fill, since ending one (joining the warps' parts, writing the outcome) takes time too:
-// counted by keys alone, blocks of many short pairs came last.
+// How U units are dealt to n workers: worker c has units [begin(c), begin(c + 1)), each of the first
+// `more` one more than the others' `each`.  With fewer units than workers, the first U take one
+// each: a pair's parts lie in consecutive blocks.  A pair counts for more units than its keys fill,
+// since ending one (joining the warps' parts, writing the outcome) takes time too: counted by keys
+// alone, blocks of many pairs came last.
 struct Deal {
     int64_t U, each;
     int more;
 
-    __device__ __forceinline__ explicit Deal(int64_t units)
-        : U(units), each(units / GRID), more((int)(units % GRID)) {}
+    Deal() = default;
+    __device__ __forceinline__ Deal(int64_t units, int n)
+        : U(units), each(units / n), more((int)(units % n)) {}
     __device__ __forceinline__ int64_t begin(int c) const { return each * c + min(c, more); }
-    // The block that holds unit x.
-    __device__ __forceinline__ int block_of(int64_t x) const {
+    // The worker that holds unit x.
+    __device__ __forceinline__ int worker_of(int64_t x) const {
         const int64_t head = (each + 1) * more;
         return x < head ? (int)(x / (each + 1)) : more + (int)((x - head) / each);
     }
 };
 
-// x = pr * nu + t: most often in 32 bits, which take a fifth of the time of a division in 64.
-__device__ __forceinline__ void pair_of(int64_t x, int nu, int& pr, int& t) {
-    if (x <= INT_MAX) {
-        pr = (int)x / nu;
-        t = (int)x % nu;
-    } else {
-        pr = (int)(x / nu);
-        t = (int)(x % nu);
-    }
+// Units that sequence b is dealt as: of each pair its keys' and those of its end.
+template <class M>
+__device__ __forceinline__ int64_t dealt_units(const Params& p, int b, bool& shorts) {
+    uint32_t first, len;
+    key_range(p, b, first, len);
+    shorts = len > first && is_short<M>(first, len);
+    return len == first ? 0
+                        : (int64_t)(units_between(first, len) + end_units<M>()) * (p.pool.H * p.QG);
 }
 
 struct DealSmem {
-    int64_t scan[NW], unit;
-    int b;
+    int64_t longs[NW], shorts[NW], unit[NW + 1];
+    int n_short[NW], b[NW + 1];
 };
 
-// Units that sequence b is dealt as: of each pair its keys' and those of its end.
-template <class M>
-__device__ __forceinline__ int64_t dealt_units(const Params& p, int b) {
-    const int nu = units_of(p, b);
-    return nu ? (int64_t)(nu + end_units<M>()) * (p.pool.H * p.QG) : 0;
+// What is dealt to a block and to this warp of it: units of long pairs and of short ones, the
+// sequence of the first of them, and that one's first unit.
+struct Share {
+    Deal longs, shorts;
+    int long_b, short_b;         // -1: none
+    int64_t long_b_unit, short_b_unit;
+    Kind kind;                   // of the pairs dealt to blocks: LONG, or ANY where all are
+};
+
+// Inclusive sum of x over the warp's lanes.
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, x, o);
+        if ((threadIdx.x & 31) >= o) x += y;
+    }
+    return x;
 }
 
-// The deal, and the place of the first unit of block c: its sequence b, and the first unit of that.  Called by all NT threads; without units for block c, b = -1.
 template <class M>
-__device__ __forceinline__ Deal deal_of(const Params& p, int c, DealSmem& sm, int& b,
-                                        int64_t& unit) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int B = p.table.S, per = (B + NT - 1) / NT;
-    const int b1 = min(B, (tid + 1) * per);
-    int64_t mine = 0;
-    for (int i = tid * per; i < b1; ++i) mine += dealt_units<M>(p, i);
-    int64_t incl = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += x;
+__device__ __forceinline__ Share share_of(const Params& p, DealSmem& sm) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+    const int B = p.table.S, pairs_b = p.pool.H * p.QG, per = (B + NT - 1) / NT;
+    const int b0 = tid * per, b1 = min(B, b0 + per);
+    // short pairs go to warps where there are enough to go round, else to blocks like the others
+    bool by_warps = M::BY_WARPS;
+    int64_t longs = 0, shorts = 0;                // units of this thread's sequences
+    int n_short = 0;
+    for (int i = b0; i < b1; ++i) {
+        bool is;
+        const int64_t x = dealt_units<M>(p, i, is);
+        is &= by_warps;
+        longs += is ? 0 : x;
+        shorts += is ? x : 0;
+        n_short += is;
     }
-    if (lane == 31) sm.scan[warp] = incl;
+    const int64_t longs_upto = warp_scan(longs);
+    if (lane == 31) sm.longs[warp] = longs_upto;
+    int64_t shorts_upto = 0;
+    if (by_warps) {
+        shorts_upto = warp_scan(shorts);
+        n_short = __reduce_add_sync(~0u, n_short);
+        if (lane == 31) {
+            sm.shorts[warp] = shorts_upto;
+            sm.n_short[warp] = n_short;
+        }
+    }
     __syncthreads();
-    int64_t U = 0, before = incl - mine;
+    int64_t longs_before = longs_upto - longs, longs_all = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += sm.scan[w];
-        U += sm.scan[w];
+        if (w < warp) longs_before += sm.longs[w];
+        longs_all += sm.longs[w];
     }
-    const Deal d(U);
-    b = -1;
-    unit = 0;
-    if (c >= U) return d;
-    const int64_t u = d.begin(c);
-    if (before <= u && u < before + mine) {
-        int64_t at = before;
-        for (int i = tid * per; i < b1; ++i) {
-            const int64_t x = per == 1 ? mine : dealt_units<M>(p, i);
+    int64_t shorts_before = shorts_upto - shorts, shorts_all = 0;
+    if (by_warps) {
+        n_short = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) shorts_before += sm.shorts[w];
+            shorts_all += sm.shorts[w];
+            n_short += sm.n_short[w];
+        }
+        by_warps = (int64_t)n_short * pairs_b >= MIN_SHORT;
+        if (!by_warps) {
+            longs += shorts;
+            longs_before += shorts_before;
+            longs_all += shorts_all;
+            shorts_all = 0;
+        }
+    }
+    Share r = {Deal(longs_all, GRID), Deal(shorts_all, GRID * NW), -1, -1, 0, 0,
+               by_warps ? LONG : ANY};
+    // the thread that holds the first unit of a share says where it is
+    auto find = [&](int64_t u, int64_t at, int64_t mine, bool want, int slot) {
+        if (u < at || u >= at + mine) return;
+        for (int i = b0; i < b1; ++i) {
+            bool is;
+            const int64_t x = per == 1 ? mine : dealt_units<M>(p, i, is);
+            if (per > 1 && by_warps && is != want) continue;
             if (u < at + x) {
-                sm.b = i;
-                sm.unit = at;
-                break;
+                sm.b[slot] = i;
+                sm.unit[slot] = at;
+                return;
             }
             at += x;
         }
-    }
+    };
+    if (c < longs_all) find(r.longs.begin(c), longs_before, longs, false, NW);
+    if (by_warps)
+#pragma unroll 1
+        for (int w = 0; w < NW; ++w)
+            if (c * NW + w < shorts_all)
+                find(r.shorts.begin(c * NW + w), shorts_before, shorts, true, w);
     __syncthreads();
-    b = sm.b;
-    unit = sm.unit;
-    return d;
+    if (c < longs_all) {
+        r.long_b = sm.b[NW];
+        r.long_b_unit = sm.unit[NW];
+    }
+    if (c * NW + warp < shorts_all) {
+        r.short_b = sm.b[warp];
+        r.short_b_unit = sm.unit[warp];
+    }
+    return r;
 }
 
+// A warp's walk over the tiles that it is to load.  A tile's page-table entries are read when it
+// enters the queue `ahead`, two tiles before they are needed: one latency for all of a ring's first
+// tiles.
 template <class M>
-__global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params p) {
-    using T = typename M::T;
-    constexpr int D = M::D, KT = M::KT, ROWB = M::ROWB, CPR = ROWB / 16;
-    constexpr int QC = (M::ROWS * CPR + NT - 1) / NT;      // pieces of the queries a thread moves
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float wm[NW][M::ROWS], wl[NW][M::ROWS];
-    __shared__ const float* wput[NW];
-    __shared__ DealSmem deal_smem;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned char* ring = smem + warp * RING;
-    unsigned char* qs = smem + NW * RING;
-    unsigned char* scratch = qs + M::QBYTES + warp * M::SCRATCH;
-    wait_for_previous();
-    let_next_start();
-    Segment seg;
-    int64_t b_unit;
-    const Deal deal = deal_of<M>(p, blockIdx.x, deal_smem, seg.b, b_unit);
-    if (tid == 0) p.headers[blockIdx.x] = {0, 0, 0};
-    if (seg.b < 0) return;
-    const int64_t u0 = deal.begin(blockIdx.x), u1 = deal.begin(blockIdx.x + 1);
-    key_range(p, seg.b, seg.first, seg.len);
-    seg.nu = units_between(seg.first, seg.len);
-    seg.u = u0;
-    seg.last = end_units<M>();
-    pair_of(u0 - b_unit, seg.nu + seg.last, seg.pr, seg.t0);
-    seg.t1 = (int)min((int64_t)seg.nu, seg.t0 + (u1 - u0));
-    // a range that begins among the units of an end, and maybe holds nothing else
-    if (seg.t0 >= seg.nu && !seg.next(p, u1)) return;
+struct Loader {
+    static constexpr int KT = M::KT, ROWB = M::ROWB, CPR = ROWB / 16;
 
-    // A segment's queries: read one segment ahead, put into shared memory when it begins.
-    uint4 qn[QC];
-    auto read_q = [&](const Segment& s) {
-        const int h = s.pr / p.QG, qg = s.pr % p.QG;
-        const int rows = min(M::ROWS, p.G - qg * M::ROWS);
-        const T* q = static_cast<const T*>(p.q) +
-                     ((int64_t)s.b * p.Hq + h * p.G + qg * M::ROWS) * D;
-#pragma unroll
-        for (int i = 0; i < QC; ++i) {
-            const int x = tid + i * NT;
-            qn[i] = x < rows * CPR ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
-        }
-    };
-    auto put_q = [&]() {
-#pragma unroll
-        for (int i = 0; i < QC; ++i) {
-            const int x = tid + i * NT;
-            if (x < M::ROWS * CPR)
-                *reinterpret_cast<uint4*>(qs + M::q_place(x / CPR, x % CPR)) = qn[i];
-        }
-    };
-    read_q(seg);
-
-    // The tiles to load next.  A tile's page-table entries are read when it enters this queue, two
-    // tiles before they are needed: one latency for all of a ring's first tiles.
     struct Tile {
         int64_t head;            // bytes from a slot to its head's row
         uint32_t at, end;        // its first key, and the end of its segment (at >= end: no tile)
         int id;                  // of lane's key: its page
     };
+
     Tile ahead[S - 1] = {};
-    Segment ls = seg;
-    uint32_t at = ls.key0() + warp * KT, end = ls.key1();
-    bool more = true;
-    const int page_shift = p.pool.page_shift;
-    auto look_up = [&](Tile& t) {
+    Segment<M> seg;
+    int64_t u1;
+    uint32_t at, end, skip, step;   // this warp's first tile of a segment, and from one to the next
+    Kind kind;
+    bool more;
+
+    __device__ __forceinline__ Loader(const Params& p, const Segment<M>& first, Kind k, int64_t end_unit,
+                                      uint32_t skip_, uint32_t step_, int lane)
+        : seg(first), u1(end_unit), at(first.key0() + skip_), end(first.key1()), skip(skip_),
+          step(step_), kind(k), more(true) {
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) look_up(p, ahead[i], lane);
+    }
+
+    __device__ __forceinline__ void look_up(const Params& p, Tile& t, int lane) {
         while (more && at >= end) {
-            more = ls.next(p, u1);
-            at = ls.key0() + warp * KT;
-            end = ls.key1();
+            more = seg.next(p, kind, u1);
+            at = seg.key0() + skip;
+            end = seg.key1();
         }
         t.at = at;
         t.end = more ? end : 0;
-        t.head = ls.pr / p.QG * p.pool.sh;
+        t.head = seg.pr / p.QG * p.pool.sh;
         t.id = -1;
         if (lane < KT && at + lane < t.end)
-            t.id = p.table.entries[ls.b * p.table.stride + ((at + lane) >> page_shift)];
-        at += NW * KT;
-    };
-    // Load the first of them, and take up another: a bit for every key that counts.
-    auto load = [&](int stage) {
+            t.id = p.table.entries[seg.b * p.table.stride + ((at + lane) >> p.pool.page_shift)];
+        at += step;
+    }
+
+    // Load the first tile of the queue, and take up another: a bit for every key that counts.
+    __device__ __forceinline__ unsigned load(const Params& p, unsigned char* stage, int lane) {
         const Tile t = ahead[0];
         unsigned ok = 0;
         if (t.at < t.end) {
@@ -669,14 +743,14 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
             const bool good = in && (unsigned)t.id < (unsigned)p.pool.n_pages;
             if (in && !good) paged_flag(p.status, GRET_PAGED_BAD_PAGE);
             ok = __ballot_sync(~0u, good);
-            const int64_t off = good ? t.id * p.pool.sp +
-                                           ((t.at + lane) & ((1u << page_shift) - 1)) * p.pool.st +
-                                           t.head
-                                     : 0;
+            const int64_t off =
+                good ? t.id * p.pool.sp +
+                           ((t.at + lane) & ((1u << p.pool.page_shift) - 1)) * p.pool.st + t.head
+                     : 0;
 #pragma unroll
             for (int i = 0; i < S - 2; ++i) ahead[i] = ahead[i + 1];
-            look_up(ahead[S - 2]);
-            const uint32_t to = sm100::smem_u32(ring + stage * 2 * HALF);
+            look_up(p, ahead[S - 2], lane);
+            const uint32_t to = sm100::smem_u32(stage);
             const int c = lane % CPR;
 #pragma unroll
             for (int i = 0; i < KT * CPR / 32; ++i) {
@@ -690,25 +764,148 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         return ok;
-    };
+    }
+};
+
+// Four dimensions of an output row, and its lse from maximum (log2) and sum.
+template <typename T>
+__device__ __forceinline__ void put_out(const Params& p, int64_t head, int D, int e, const float (&a)[4],
+                                        float mx, float z) {
+    T* o = static_cast<T*>(p.o) + head * D + e;
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) look_up(ahead[i]);
+    for (int x = 0; x < 4; ++x) o[x] = from_f32<T>(a[x] / z);
+    if (p.lse && e == 0) p.lse[head] = (mx + log2f(z)) * LN2;
+}
+
+// The short pairs dealt to this warp, one after another, each from its first key to its output.  Two
+// stages of the ring hold tiles, the third the queries.
+template <class M>
+__device__ __forceinline__ void work_by_warp(const Params& p, M& math, const Share& share,
+                                             unsigned char* ring, unsigned char* scratch, float* wm,
+                                             float* wl) {
+    using T = typename M::T;
+    constexpr int D = M::D, CPR = M::ROWB / 16, STAGE = 2 * HALF;
+    constexpr int PR = M::ROWS / M::NPASS, FIT = STAGE / (PR * D * 4);
+    const int lane = threadIdx.x & 31, worker = blockIdx.x * NW + (threadIdx.x >> 5);
+    const int64_t u1 = share.shorts.begin(worker + 1);
+    Segment<M> seg;
+    if (share.short_b < 0 || !seg.start(p, SHORT, share.short_b, share.short_b_unit,
+                                        share.shorts.begin(worker), u1))
+        return;
+    unsigned char* qs = ring + 2 * STAGE;
+    Loader<M> loader(p, seg, SHORT, u1, 0, M::KT, lane);
+    unsigned ok = loader.load(p, ring, lane);
+    int stage = 0;
+    for (bool go = true; go;) {
+        const int rows = seg.rows(p);
+        const int64_t head = seg.head(p);
+        const unsigned char* q =
+            static_cast<const unsigned char*>(p.q) + head * M::ROWB;
+        for (int x = lane; x < M::ROWS * CPR; x += 32)
+            cp_async_16_or_zero(sm100::smem_u32(qs + M::q_place(x / CPR, x % CPR)),
+                                x < rows * CPR ? q + x * 16 : q, x < rows * CPR ? 16 : 0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const uint32_t key0 = seg.key0(), key1 = seg.key1();
+        for (uint32_t k = key0; k < key1; k += M::KT) {
+            const unsigned ok_next = loader.load(p, ring + (stage ^ 1) * STAGE, lane);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
+            if (k == key0) math.begin(qs, lane);
+            const unsigned char* t = ring + stage * STAGE;
+            math.tile(t, t + HALF, qs, scratch, ok, p.scale_log2, lane);
+            __syncwarp();
+            ok = ok_next;
+            stage ^= 1;
+        }
+        math.end(wm, wl, lane);
+        // the tile last worked on has made room
+        float* buf = reinterpret_cast<float*>(ring + (stage ^ 1) * STAGE);
+#pragma unroll 1
+        for (int pass = 0; pass < M::NPASS; pass += FIT) {
+            for (int i = 0; i < FIT && pass + i < M::NPASS; ++i)
+                math.put(pass + i, buf + i * PR * D, lane);
+            __syncwarp();
+            const int row0 = pass * PR, n = min(rows - row0, FIT * PR);
+            for (int i = lane; i < n * (D / 4); i += 32) {
+                const int r = i / (D / 4), e = i % (D / 4) * 4;
+                const float4 x = *reinterpret_cast<const float4*>(buf + put_place(D, r, e));
+                const float a[4] = {x.x, x.y, x.z, x.w};
+                put_out<T>(p, head + row0 + r, D, e, a, wm[row0 + r], wl[row0 + r]);
+            }
+            __syncwarp();
+        }
+        go = seg.next(p, SHORT, u1);
+    }
+}
+
+template <class M>
+__global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params p) {
+    using T = typename M::T;
+    constexpr int D = M::D, KT = M::KT, CPR = M::ROWB / 16;
+    constexpr int QC = (M::ROWS * CPR + NT - 1) / NT;      // pieces of the queries a thread moves
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float wm[NW][M::ROWS], wl[NW][M::ROWS];
+    __shared__ const float* wput[NW];
+    __shared__ DealSmem deal_smem;
+    __shared__ Deal longs;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+    unsigned char* ring = smem + warp * RING;
+    unsigned char* qs = smem + NW * RING;
+    unsigned char* scratch = qs + M::QBYTES + warp * M::SCRATCH;
+    wait_for_previous();
+    let_next_start();
+    const Share share = share_of<M>(p, deal_smem);
+    if (tid == 0) {
+        p.headers[c] = {0, 0, 0};
+        longs = share.longs;
+    }
+    M math;
+    if (M::BY_WARPS && share.kind == LONG) {
+        work_by_warp<M>(p, math, share, ring, scratch, wm[warp], wl[warp]);
+        __syncthreads();
+    }
+    const int64_t u1 = share.longs.begin(c + 1);
+    Segment<M> seg;
+    if (share.long_b < 0 || !seg.start(p, share.kind, share.long_b, share.long_b_unit,
+                                       share.longs.begin(c), u1))
+        return;
+
+    // A segment's queries: read one segment ahead, put into shared memory when it begins.
+    uint4 qn[QC];
+    auto read_q = [&](const Segment<M>& s) {
+        const T* q = static_cast<const T*>(p.q) + s.head(p) * D;
+        const int n = s.rows(p) * CPR;
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            const int x = tid + i * NT;
+            qn[i] = x < n ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto put_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            const int x = tid + i * NT;
+            if (x < M::ROWS * CPR)
+                *reinterpret_cast<uint4*>(qs + M::q_place(x / CPR, x % CPR)) = qn[i];
+        }
+    };
+    read_q(seg);
+    Loader<M> loader(p, seg, share.kind, u1, warp * KT, NW * KT, lane);
     unsigned ok[S];
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) ok[i] = load(i);
+    for (int i = 0; i < S - 1; ++i) ok[i] = loader.load(p, ring + i * 2 * HALF, lane);
     int stage = 0;
     put_q();
     __syncthreads();
 
-    M math;
     for (bool go = true; go;) {
-        Segment nx = seg;
-        go = nx.next(p, u1);
+        Segment<M> nx = seg;
+        go = nx.next(p, share.kind, u1);
         if (go) read_q(nx);
-        math.begin(qs, scratch, lane);
+        math.begin(qs, lane);
         const uint32_t key1 = seg.key1();
         for (uint32_t k = seg.key0() + warp * KT; k < key1; k += NW * KT) {
-            ok[S - 1] = load(stage == 0 ? S - 1 : stage - 1);
+            ok[S - 1] = loader.load(p, ring + (stage == 0 ? S - 1 : stage - 1) * 2 * HALF, lane);
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
             __syncwarp();
             const unsigned char* t = ring + stage * 2 * HALF;
@@ -719,16 +916,13 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
             stage = stage == S - 1 ? 0 : stage + 1;
         }
         // join the warps' parts, through the ring's one stage that no load is under way to
-        const int h = seg.pr / p.QG, qg = seg.pr % p.QG;
-        const int rows = min(M::ROWS, p.G - qg * M::ROWS);
-        const int64_t head0 = (int64_t)seg.b * p.Hq + h * p.G + qg * M::ROWS;   // first query row
+        const int rows = seg.rows(p);
+        const int64_t head0 = seg.head(p);
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nu;
-        Part<M::ROWS, D>* part =
-            static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * blockIdx.x + (seg.t0 == 0);
+        Part<M::ROWS, D>* part = static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * c + (seg.t0 == 0);
         if (!whole && seg.t0 == 0 && tid == 0)
-            p.headers[blockIdx.x] = {
-                (int32_t)head0, (int16_t)rows,
-                (int16_t)(deal.block_of(seg.u + seg.nu - 1) - (int)blockIdx.x + 1)};
+            p.headers[c] = {(int32_t)head0, (int16_t)rows,
+                            (int16_t)(longs.worker_of(seg.u + seg.nu - 1) - c + 1)};
         // in passes of as many rows as the stage holds; when the block ends here, nothing is under
         // way, and one pass does
         constexpr int PR = M::ROWS / M::NPASS;             // rows of a tile of queries
@@ -764,10 +958,7 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
                     z += wl[w][row] * f;
                 }
                 if (whole) {
-                    T* o = static_cast<T*>(p.o) + (head0 + row) * D + e;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) o[x] = from_f32<T>(a[x] / z);
-                    if (p.lse && e == 0) p.lse[head0 + row] = (mx + log2f(z)) * LN2;
+                    put_out<T>(p, head0 + row, D, e, a, mx, z);
                 } else {
                     *reinterpret_cast<float4*>(&part->a[row][e]) =
                         make_float4(a[0], a[1], a[2], a[3]);
@@ -885,9 +1076,17 @@ template <class M>
 cudaError_t launch(Params& p, cudaStream_t stream) {
     constexpr int smem = NW * (RING + M::SCRATCH) + M::QBYTES;
     p.QG = (p.G + M::ROWS - 1) / M::ROWS;
-    cudaError_t e = allow_smem<paged_attn_kernel<M>>(smem, smem);
-    if (e != cudaSuccess) return e;
-    e = launch_early(paged_attn_kernel<M>, dim3(GRID), NT, smem, stream, p);
+    cudaError_t e;
+    if (M::SPARE && (int64_t)p.table.S * p.pool.H * p.QG >= MIN_SHORT) {
+        using W = typename std::conditional<M::SPARE, ByWarps<M>, M>::type;
+        e = allow_smem<paged_attn_kernel<W>>(smem, smem);
+        if (e == cudaSuccess)
+            e = launch_early(paged_attn_kernel<W>, dim3(GRID), NT, smem, stream, p);
+    } else {
+        e = allow_smem<paged_attn_kernel<M>>(smem, smem);
+        if (e == cudaSuccess)
+            e = launch_early(paged_attn_kernel<M>, dim3(GRID), NT, smem, stream, p);
+    }
     if (e != cudaSuccess) return e;
     return launch_early(paged_join_kernel<M>, dim3(GRID, p.G < JOIN_Y ? p.G : JOIN_Y), NT, 0,
                         stream, p);

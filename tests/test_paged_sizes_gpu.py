@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from paged_model import Cache
+from paged_model import Cache, attention
+from parity import bf16_half_ulp
 from test_paged_gpu import BF16, F32, Dev, check, filled, i32, lib, queries, resize
 
 pytestmark = pytest.mark.gpu
@@ -61,6 +62,60 @@ def test_attention_borders(seed):
     dev, q = Dev(c, seed % 2 == 1), queries(B, H * G, d, dtype, seed)
     o, lse = dev.decode(q)
     check(c, q, o, lse)
+
+
+@pytest.mark.parametrize("dtype,H,G,d,page,hm,window", [
+    (BF16, 8, 3, 128, 16, False, 0), (BF16, 4, 8, 64, 8, True, 0), (BF16, 3, 16, 64, 32, False, 30),
+    (BF16, 5, 24, 64, 16, False, 0), (BF16, 6, 1, 128, 1, True, 100), (F32, 4, 4, 128, 16, False, 0),
+    (F32, 3, 7, 128, 8, True, 0), (F32, 4, 12, 64, 16, False, 50), (F32, 3, 20, 64, 64, False, 0),
+    (BF16, 3, 12, 128, 16, False, 0), (F32, 3, 16, 128, 16, False, 0), (BF16, 4, 40, 64, 16, True, 0),
+])
+def test_attention_many_short_pairs(dtype, H, G, d, page, hm, window):
+    """Hundreds of short sequences, of every length around what a warp takes on by itself, among
+    empty ones and long ones; then few short ones among many long, and only short ones."""
+    rng = np.random.default_rng(H * G + d)
+    tile = (32 if d == 64 else 16) // (2 if dtype == F32 else 1)
+    most = 8 * tile
+    near = np.array([1, 2, tile - 1, tile, tile + 1, 3 * tile + 1, most - 1, most, most + 1, most + 7])
+    for mix in range(3):
+        B = 330
+        lens = rng.choice(near if mix < 2 else near[:8], B)
+        if mix == 0:
+            lens[rng.random(B) < 0.1] = 0
+            lens[rng.permutation(B)[:5]] = rng.integers(500, 3000, 5)
+        if mix == 1:
+            lens[rng.random(B) < 0.8] = most + 5
+        c = filled(lens.tolist(), page, H, d, dtype, seed=70 + mix)
+        dev, q = Dev(c, hm), queries(B, H * G, d, dtype, mix)
+        o, lse = dev.decode(q, window=window)
+        check(c, q, o, lse, window)
+        again, _ = dev.decode(q, window=window)
+        assert torch.equal(o, again) and int(dev.status) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_attention_short_pairs_bad_pages(dtype):
+    """Bad pages and lengths in sequences that single warps work on: left out and reported."""
+    G = lib()
+    c = filled([20] * 300, 8, 2, 64, dtype, seed=80)
+    dev, q = Dev(c), queries(300, 6, 64, dtype, 80)
+    dev.table[7, 1], dev.table[250, 2] = -1, len(c.ref)
+    dev.table[9, 0], dev.lens[9] = 10 ** 9, 8          # no key left
+    dev.lens[100] = -4
+    status = dev.status
+    o, lse = dev.decode(q)
+    assert G.gret_paged_status(status) == G.GRET_PAGED_BAD_PAGE | G.GRET_PAGED_BAD_LENGTH
+    same = [s for s in range(300) if s not in (7, 9, 100, 250)]
+    check(c, q, o, lse, rows=same)
+    assert (o[100] == 0).all() and (lse[100] == -float("inf")).all()
+    assert torch.isnan(o[9]).all() and (lse[9] == -float("inf")).all()
+    for s, keep in ((7, np.r_[0:8, 16:20]), (250, np.r_[0:16])):
+        k, v = c.tokens(s, 0, 20)
+        ro, rl, eo, el = attention(q[s].cpu(), k[keep], v[keep], 64 ** -0.5)
+        half = torch.from_numpy(bf16_half_ulp(ro.numpy()) * 2) if dtype == BF16 \
+            else ro.abs() * 2.0 ** -24
+        assert ((o[s].cpu().double() - ro).abs() <= eo + half).all()
+        assert ((lse[s].cpu().double() - rl).abs() <= el).all()
 
 
 # -------------------------------------------------------------------------------- upkeep
