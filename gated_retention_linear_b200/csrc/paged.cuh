@@ -131,8 +131,8 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
-// Dynamic shared memory of `bytes`, at most `most`, for a kernel: up to 24 KB beside its own arrays need
-// no leave; for more it is asked once on each of the first 64 devices.
+// Dynamic shared memory of `bytes`, at most `most`, for a kernel: up to 24 KB beside its own arrays
+// need no leave; for more it is asked once on each of the first 64 devices.
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes, int most) {
     static std::atomic<uint64_t> given{0};

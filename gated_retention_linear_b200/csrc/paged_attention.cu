@@ -8,26 +8,32 @@
 //     m = max m_i,  l = sum e^(m_i - m) l_i,  o = sum e^(m_i - m) a_i / l.
 //
 // Bound: HBM, 2 n d values a (sequence, kv head) read once, 2 G flops a value.  That little
-// arithmetic leaves the tensor cores idle for most of the time in any form, so the form is chosen
-// for the loads: every warp runs its own ring of cp.async tiles (KT keys and values of one head, 8
-// KB), two of them always in flight behind the one being worked on and across the borders of
-// sequences, with no barrier between warps but where a (sequence, head) ends; page-table entries
-// are read one tile ahead of that.  16-byte pieces gathered by lanes take any page size and any
-// stride, where a bulk copy would want one tensor map a layout and at least a page of tokens.
+// arithmetic leaves the tensor cores idle for most of the time in any form (14 % busy at G = 3), so
+// the form is chosen for the loads: every warp runs its own ring of cp.async tiles (KT keys and
+// values of one head, 8 KB), two of them always in flight behind the one being worked on and across
+// the borders of sequences, with no barrier between warps but where a (sequence, head) ends;
+// page-table entries are read two tiles ahead of that.  16-byte pieces gathered by lanes take any
+// page size and any stride, where a bulk copy would want one tensor map a layout and at least a page
+// of tokens. Measured, 8 kv heads of 128 in bf16, G = 3: 64 sequences of 200 to 32768 tokens 270 us
+// (6.5 TB/s, what a plain copy reaches), 2 of 524288 645 us; one of 4096 8.9 us, of which 6.7 go by
+// with no more than 100 tokens: two launches, and the chain length -> page -> keys -> parts -> join.
 //
-// bf16: keys are the M side of the product and the query heads of the group the N side (8 to 32,
-// padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows;
-// p is split into two bf16 parts (hi + lo = p up to 2^-16) because one part alone would put its
-// rounding of 2^-9 on every weight, and O^T = V^T P^T.  Both read their 16-bit tiles from shared
-// memory by ldmatrix, the accumulators stay in registers.  fp32: products in fp32 on the CUDA
-// cores, a lane a key for the scores and a lane four dimensions for the values.
+// bf16: keys are the M side of the product and the query heads of the group the N side (8 to 24,
+// padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows; p is split
+// into two bf16 parts (hi + lo = p up to 2^-16) because one part alone would put its rounding of
+// 2^-9 on every weight, and O^T = V^T P^T.  Both read their 16-bit tiles from shared memory by
+// ldmatrix, the accumulators stay in registers.  From 16 heads a group on the products and the
+// softmax no longer hide behind the loads: 24 heads on one kv head run at 0.58 of the copy
+// bandwidth, 12 of 128 at 0.88.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
+// the scores and a lane four dimensions for the values; 0.94 of the copy bandwidth at G = 3, 0.79 at
+// 8; at 16 (0.45) the queries' reads from shared memory bound it.
 //
-// The work is cut into units of UNIT keys of one (sequence, kv head, group of query rows); the
-// units of the whole batch are dealt out evenly over the grid, in order, so that one long
+// The work is cut into units of UNIT keys of one (sequence, kv head, group of query rows), a pair;
+// the units of the whole batch are dealt out evenly over the grid, in order, so that one long
 // sequence spreads over every SM and a ragged batch stays balanced without the host knowing the
 // lengths.  A block whose range ends inside a (sequence, head) writes its part to the workspace;
-// a second kernel joins the parts in block order, so that results do not depend on timing.  It is
-// launched as a dependent of the first one, whose end it waits for on the device.
+// a second kernel joins the parts in block order, so that results do not depend on timing.  Batches
+// of many short pairs go to single warps instead (ByWarps).
 #include <cuda_bf16.h>
 #include <limits.h>
 #include <math.h>
@@ -59,8 +65,8 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
 // What the join needs of block c: of the pair whose first part block c holds, and not the rest, the
-// first query row, the rows, and the blocks that hold parts of it (block c's tail slot, then the head
-// slots of the next).  No such pair: no rows.
+// first query row, the rows, and the blocks that hold parts of it (block c's tail slot, then the
+// head slots of the next).  No such pair: no rows.
 struct Header {
     int32_t head;
     int16_t rows, parts;
@@ -308,8 +314,8 @@ struct Bf16Math {
                 for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        to[put_place(D, 2 * (lane & 3) + (e & 1), 16 * k + lane / 4 + (e >> 1) * 8)] =
-                            acc[i][k][e];
+                        to[put_place(D, 2 * (lane & 3) + (e & 1),
+                                     16 * k + lane / 4 + (e >> 1) * 8)] = acc[i][k][e];
     }
 };
 
@@ -442,12 +448,12 @@ struct F32Math {
     }
 };
 
-// The same with short pairs worked on by single warps.  A block takes 1.5 us and more to end a pair, and
-// one warp little longer for a short one altogether, while the block's others do as much: 187 x 16 pairs
-// of 2 keys 32 -> 16 us, 192 x 16 of 70 keys of 64 dimensions 32 -> 22.  A kernel of its own, for
-// batches that may have enough such pairs: others would be 3 to 6 % slower for the code that they have
-// no use for.  Not where the rows' sums leave no registers to spare (SPARE): there the kernel would be
-// 9 % slower on batches that are long after all.
+// The same with short pairs worked on by single warps.  A block takes 1.5 us and more to end a pair,
+// and one warp little longer for a short one altogether, while the block's others do as much: 187 x
+// 16 pairs of 2 keys 32 -> 16 us, 192 x 16 of 70 keys of 64 dimensions 32 -> 22.  A kernel of its
+// own, for batches that may have enough such pairs: others would be 3 to 6 % slower for the code
+// that they have no use for.  Not where the rows' sums leave no registers to spare (SPARE): there
+// the kernel would be 9 % slower on batches that are long after all.
 template <class M>
 struct ByWarps : M {
     static constexpr bool BY_WARPS = true;
@@ -476,7 +482,8 @@ __device__ __forceinline__ int units_of(const Params& p, int b) {
     return units_between(first, len);
 }
 
-// What ending a pair costs, in units: 1.5 us, and 1.2 for each 8 rows more, when a block reads 22 KB a us.
+// What ending a pair costs, in units: 1.5 us, and 1.2 for each 8 rows more, when a block reads 22 KB
+// a us.
 template <class M>
 constexpr int end_units() {
     constexpr int unit_ns = UNIT * 2 * M::ROWB * 1000 / 22000, end_ns = 300 + 1200 * M::NPASS;
@@ -501,8 +508,8 @@ struct Segment {
     uint32_t first, len;
     int b, pr, nu, t0, t1;
 
-    // At unit u, in sequence b_, whose units begin at b_unit, of those dealt up to u1; false if there
-    // are no keys in [u, u1).
+    // At unit u, in sequence b_, whose units begin at b_unit, of those dealt up to u1; false if
+    // there are no keys in [u, u1).
     __device__ __forceinline__ bool start(const Params& p, Kind kind, int b_, int64_t b_unit,
                                           int64_t u_, int64_t u1) {
         b = b_;
@@ -520,7 +527,9 @@ struct Segment {
         t1 = (int)min((int64_t)nu, t0 + (u1 - u));
         // short pairs belong whole to the warp that their first unit is dealt to; a range may also
         // begin among the units of an end
-        return t0 >= (kind == SHORT ? 1 : nu) ? next(p, kind, u1) : kind != SHORT || (t1 = nu, true);
+        if (t0 >= (kind == SHORT ? 1 : nu)) return next(p, kind, u1);
+        if (kind == SHORT) t1 = nu;
+        return true;
     }
     __device__ __forceinline__ uint32_t key0() const { return first + (uint32_t)t0 * UNIT; }
     __device__ __forceinline__ uint32_t key1() const {
@@ -711,8 +720,8 @@ struct Loader {
     Kind kind;
     bool more;
 
-    __device__ __forceinline__ Loader(const Params& p, const Segment<M>& first, Kind k, int64_t end_unit,
-                                      uint32_t skip_, uint32_t step_, int lane)
+    __device__ __forceinline__ Loader(const Params& p, const Segment<M>& first, Kind k,
+                                      int64_t end_unit, uint32_t skip_, uint32_t step_, int lane)
         : seg(first), u1(end_unit), at(first.key0() + skip_), end(first.key1()), skip(skip_),
           step(step_), kind(k), more(true) {
 #pragma unroll
@@ -769,8 +778,8 @@ struct Loader {
 
 // Four dimensions of an output row, and its lse from maximum (log2) and sum.
 template <typename T>
-__device__ __forceinline__ void put_out(const Params& p, int64_t head, int D, int e, const float (&a)[4],
-                                        float mx, float z) {
+__device__ __forceinline__ void put_out(const Params& p, int64_t head, int D, int e,
+                                        const float (&a)[4], float mx, float z) {
     T* o = static_cast<T*>(p.o) + head * D + e;
 #pragma unroll
     for (int x = 0; x < 4; ++x) o[x] = from_f32<T>(a[x] / z);
@@ -974,8 +983,8 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
     }
 }
 
-// Row r of the n parts, to query row `head`: a warp a quarter of the parts, a lane D / 32 dimensions.
-// All that a row is made of is on its way before any of it is looked at, up to 32 parts.
+// Row r of the n parts, to query row `head`: a warp a quarter of the parts, a lane D / 32
+// dimensions. All that a row is made of is on its way before any of it is looked at, up to 32 parts.
 template <class M>
 __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M::D>* parts, int n,
                                          int r, int64_t head) {
@@ -1093,7 +1102,8 @@ cudaError_t launch(Params& p, cudaStream_t stream) {
 }
 
 // Query rows a block works on at a time: all G heads of a group where they fit, else the fewest
-// equal passes over the keys (each pass reads them again), in steps of 8 rows for bf16 and 4 for fp32.
+// equal passes over the keys (each pass reads them again), in steps of 8 rows for bf16 and 4 for
+// fp32.
 int rows_of(bool bf16, int G) {
     const int most = bf16 ? MAXROWS_BF16 : MAXROWS_F32, step = bf16 ? 8 : 4;
     const int passes = (G + most - 1) / most, rows = (G + passes - 1) / passes;
@@ -1138,7 +1148,8 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.headers = static_cast<Header*>(a.workspace);
     p.parts = static_cast<unsigned char*>(a.workspace) + (GRID * sizeof(Header) + 255) / 256 * 256;
     const int rows = rows_of(a.bf16, p.G);
-    return a.d == 64 ? launch_d<64>(a.bf16, rows, p, stream) : launch_d<128>(a.bf16, rows, p, stream);
+    return a.d == 64 ? launch_d<64>(a.bf16, rows, p, stream)
+                     : launch_d<128>(a.bf16, rows, p, stream);
 }
 
 }  // namespace gret

@@ -63,7 +63,8 @@ struct Scope {
     c10::cuda::OptionalCUDAStreamGuard stream;
     gret_stream_t raw;
 
-    Scope(PyObject* given, const at::Tensor& first, std::initializer_list<const at::Tensor*> others) {
+    Scope(PyObject* given, const at::Tensor& first,
+          std::initializer_list<const at::Tensor*> others) {
         if (!first.is_cuda()) refuse(PyExc_ValueError, "paged cache tensors must be on a GPU");
         for (const at::Tensor* t : others)
             if (t && t->device() != first.device())
@@ -191,8 +192,9 @@ PyObject* attention_decode(PyObject* const* a) {
     if (given_o && (given_o->sizes() != q.sizes() || given_o->scalar_type() != q.scalar_type() ||
                     !given_o->is_contiguous()))
         refuse(PyExc_ValueError, "o must be contiguous and of q's shape and dtype");
-    if (given_lse && (given_lse->dim() != 2 || given_lse->size(0) != B || given_lse->size(1) != Hq ||
-                      given_lse->scalar_type() != at::kFloat || !given_lse->is_contiguous()))
+    if (given_lse &&
+        (given_lse->dim() != 2 || given_lse->size(0) != B || given_lse->size(1) != Hq ||
+         given_lse->scalar_type() != at::kFloat || !given_lse->is_contiguous()))
         refuse(PyExc_ValueError, "lse must be contiguous float32 [B, Hq]");
     const int32_t* lens_at = int32s(&lens, "seq_lens", B);
     int32_t* status_at = int32s(status, "status", 1);

@@ -30,8 +30,8 @@ constexpr int MAXCH = 4 * PNT;         // chunks of ref
 constexpr int GROUP = 4;               // chunks a warp counts at once
 constexpr int GRID = 148 * 4;          // blocks of the kernels that carry a plan out
 constexpr int NT = 256;
-constexpr int APPLY_SM = 6;            // of a resize's: rows wait for lists and counts, not for bandwidth
-constexpr int64_t FORK_ALONE = 1 << 17;   // pairs x table entries that one fork kernel does
+constexpr int APPLY_SM = 6;            // of a resize's an SM: its rows wait for lists and counts
+constexpr int64_t FORK_ALONE = 1 << 21;   // pairs x table entries that one fork kernel does
 
 // Exclusive sums of x and y over the block's threads, and the totals.  `sums` has 2 PNW entries.
 struct Sums {
@@ -76,9 +76,9 @@ __device__ __forceinline__ Sums block_scan(int64_t x, int y, int64_t (*sums)[2])
     return r;
 }
 
-// ref, read 16 bytes at a time whatever its alignment: quad j is the entries 4 j - skew and on, where
-// entries before the first and from P on count as taken.  Chunk c is the quads [c * step,
-// c * step + step).
+// ref, read 16 bytes at a time whatever its alignment: quad j is the entries 4 j - skew and on,
+// where entries before the first and from P on count as taken.  Chunk c is the quads [c * step, c *
+// step + step).
 struct Chunks {
     const int32_t* ref;
     int P, skew, step, n;
@@ -156,7 +156,7 @@ __device__ __forceinline__ void count_free(const Chunks& ch, int* count) {
                     for (int i = lane; i < ch.step; i += 32)
                         n[g] += free_of(ch.quad(first + g * far + i));
         }
-        if (!begun) cluster.barrier_wait();      // every block runs: its shared memory can be written
+        if (!begun) cluster.barrier_wait();      // every block runs: its shared memory is there
         begun = true;
 #pragma unroll
         for (int g = 0; g < GROUP; ++g) {
@@ -224,8 +224,8 @@ struct Pieces {
 
 // The pieces [c0, c0 + NT) of the slots below `slots` of page `from`, to page `to`, by a block.  One
 // piece of keys and one of values a thread: four blocks an SM then have 32 KB on their way, enough
-// to hide HBM's latency; with 64 or 128 KB reads and writes get in each other's way (16448 moves
-// of 64 KB: 330, 351 and 360 us).
+// to hide HBM's latency; with 64 or 128 KB reads and writes get in each other's way (16448 moves of
+// 64 KB: 330, 351 and 360 us).
 __device__ __forceinline__ void copy_pieces(const PagedPool& p, const Pieces& pc, int64_t from,
                                             int64_t to, int c0, int slots) {
     const uint32_t c = c0 + threadIdx.x;
@@ -241,9 +241,10 @@ __device__ __forceinline__ void copy_pieces(const PagedPool& p, const Pieces& pc
 
 // ---------------------------------------------------------------------------------------------
 // append: a copy of every token's row of heads to its slot.  Bound by HBM, each byte read and
-// written once; with few tokens by the chain row -> position -> page -> copy, so a warp's lanes
-// find the places of its tokens side by side, and a warp takes several only when there are more
-// tokens than warps to go round.
+// written once; with few tokens by the chain row -> position -> page -> copy, so a warp's lanes find
+// the places of its tokens side by side, and a warp takes several only when there are more tokens
+// than warps to go round.  Measured, 8 heads of 128 in bf16: 176,600 tokens 228 us (6.3 TB/s), 256
+// single tokens 2.6 us.
 
 constexpr int AP_MAXTOK = 8;           // tokens of one warp
 constexpr int AP_U = 4;                // pieces of keys, and of values, in flight a lane
@@ -320,7 +321,11 @@ __global__ void __launch_bounds__(NT) append_kernel(const PagedAppendArgs a, con
 }
 
 // ---------------------------------------------------------------------------------------------
-// resize: a plan by one cluster (who gets which page), then the whole GPU carries it out.
+// resize: a plan by one cluster (who gets which page), then the whole GPU carries it out.  Latency
+// bounds it: of a step of 256 rows on 20000 pages (10 us) the plan takes 7 (rows 1.5, counting 1.4,
+// the cluster's barrier and the sums 1.2, handing out 1.5, the launch the rest) and the copies 2.7;
+// of 1000 rows that come and go on 786433 pages (25 us) counting takes 6, 50 GB/s an SM, handing out
+// 6.
 
 constexpr int ROWS_U = 4;              // rows that a planning thread looks at at once
 
@@ -487,7 +492,8 @@ __device__ __forceinline__ void drop_page(const PagedResizeArgs& a, int id) {
 }
 
 // The entries [j0, j1) of a row, by the whole block: four a thread on their way at a time.
-__device__ __forceinline__ void drop_entries(const PagedResizeArgs& a, int32_t* row, int j0, int j1) {
+__device__ __forceinline__ void drop_entries(const PagedResizeArgs& a, int32_t* row, int j0,
+                                             int j1) {
     constexpr int U = 4;
     for (int j = j0 + threadIdx.x; j < j1; j += NT * U) {
         int id[U], had[U];
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(NT, APPLY_SM) resize_apply_kernel(const PagedR
     }
     // the copies, NT rows at a time, in steps dealt over all blocks.  pos is the old length
     const int steps = (pc.total + NT - 1) / NT;
-    int k = blockIdx.x / steps, c = blockIdx.x % steps;   // this block's next: step c of the batch's row k
+    int k = blockIdx.x / steps, c = blockIdx.x % steps;   // next: step c of the batch's row k
     const int dk = GRID / steps, dc = GRID % steps;
     for (int s0 = 0; s0 < S; s0 += NT) {
         // the batch's rows that copy, in order: all blocks have to count them alike
@@ -570,11 +576,11 @@ __global__ void __launch_bounds__(NT, APPLY_SM) resize_apply_kernel(const PagedR
 }
 
 // ---------------------------------------------------------------------------------------------
-// fork.  The copy of the table entries is bound by HBM (L2, for the rows that many share).  The
-// counts are bound by atomics on one address where many pairs share a source and each adds its 1:
-// there, of the m pairs of a source each adds m to an m-th of its pages.  That takes the pairs'
-// knowing of one another, so that the lengths, by which a pair that has no effect is known, can
-// only be set by a second kernel; small calls go without.
+// fork.  The copy of the table entries is bound by HBM (L2, for the rows that many share): 512 rows
+// of 7000 entries 10 us, 64 of 50 2.7.  The counts are bound by atomics on one address where many
+// pairs share a source and each adds its 1: there, of the m pairs of a source each adds m to an m-th
+// of its pages.  That takes the pairs' knowing of one another, so that the lengths, by which a pair
+// that has no effect is known, can only be set by a second kernel; small calls go without.
 
 // The first pair that names each row as its destination (INT_MAX: none).
 __device__ __forceinline__ void first_pairs(const PagedForkArgs& a, int* first) {
@@ -674,7 +680,8 @@ __global__ void __launch_bounds__(NT) fork_lengths_kernel(const PagedForkArgs a)
 }
 
 // ---------------------------------------------------------------------------------------------
-// compact: with L pages in use, the k-th page in use past L moves to the k-th hole below L.
+// compact: with L pages in use, the k-th page in use past L moves to the k-th hole below L.  Bound
+// by HBM but for small pools: 16400 pages of 64 KB moved in 338 us (6.3 TB/s), 240 in 11.
 
 // The plan in the workspace: {L, pages to move}, then by page: the k-th hole, the page in use of
 // rank r, the rank of a page in use past L (-1: free).
@@ -794,24 +801,28 @@ cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_early(resize_plan_kernel, dim3(CL), PNT, smem, stream, a);
     if (e != cudaSuccess) return e;
-    return launch_early(resize_apply_kernel, dim3(APPLY_SM * 148), NT, 0, stream, a, Pieces(a.pool));
+    return launch_early(resize_apply_kernel, dim3(APPLY_SM * 148), NT, 0, stream, a,
+                        Pieces(a.pool));
 }
 
 cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
+    constexpr int most_smem = PAGED_MAX_SEQS * (int)sizeof(int);
     const size_t smem = (size_t)a.table.S * sizeof(int);
     const int x = a.n < 2 * GRID ? a.n : 2 * GRID;
     cudaError_t e;
-    // Alone a block a pair, rows of up to 4 steps of a block, and no more atomics than take a
-    // microsecond or two on few addresses.
-    if (a.table.max_pages <= 4096 && (int64_t)a.n * a.table.max_pages <= FORK_ALONE) {
-        e = allow_smem<fork_kernel<false>>(smem, PAGED_MAX_SEQS * (int)sizeof(int));
+    // Without sharing out the counts: one launch, a block a pair.  Measured against two launches, in
+    // us: 64 rows of 76 entries 8 and 11, 512 of 512 11 and 13, 2000 of 1000 15 and 23, 1024 of 2048
+    // 13 and 15; but 512 of 8192 16 and 15, and one row of 32768, which only the other cuts up, 16
+    // and 11.
+    if (a.table.max_pages <= 8192 && (int64_t)a.n * a.table.max_pages <= FORK_ALONE) {
+        e = allow_smem<fork_kernel<false>>(smem, most_smem);
         if (e != cudaSuccess) return e;
         return launch_early(fork_kernel<false>, dim3(x), NT, smem, stream, a);
     }
-    e = allow_smem<fork_kernel<true>>(smem, PAGED_MAX_SEQS * (int)sizeof(int));
-    if (e == cudaSuccess) e = allow_smem<fork_lengths_kernel>(smem, PAGED_MAX_SEQS * (int)sizeof(int));
+    e = allow_smem<fork_kernel<true>>(smem, most_smem);
+    if (e == cudaSuccess) e = allow_smem<fork_lengths_kernel>(smem, most_smem);
     if (e != cudaSuccess) return e;
-    // a block a pair; with few pairs a row is cut up, in pieces of 1024 entries at least
+    // a block a pair; with few pairs a row is cut up, in pieces of 1024 entries or more
     int y = 2 * GRID / x, most = (a.table.max_pages + 1023) / 1024;
     if (y > most) y = most;
     e = launch_early(fork_kernel<true>, dim3(x, y), NT, smem, stream, a);

@@ -172,6 +172,7 @@ def test_pool_alignments(off, P):
 
 @pytest.mark.parametrize("parents,children,pages", [
     (1, 1, 5000), (2, 3, 9000), (3, 40, 4097), (2, 1300, 120), (5, 60, 2000), (4, 64, 76),
+    (4, 600, 4000), (1, 1, 9000),
 ])
 def test_fork_kinds(parents, children, pages):
     """Few long rows, many short ones, and pairs that are refused among those that share a source."""
@@ -327,3 +328,24 @@ def test_binding_scope():
     assert got is lse
     check(c, q, o2, lse, scale=1)
     check(c, q, o, G.gret_paged_attention_decode(q, dev.lens, dev.table, dev.k, dev.v, lse=True)[1])
+
+
+@pytest.mark.parametrize("dtype,B,H,G,d", [
+    (BF16, 3, 2, 3, 128), (BF16, 250, 4, 5, 64), (F32, 7, 1, 13, 64), (F32, 300, 3, 2, 128),
+])
+def test_attention_writes_its_outputs_only(dtype, B, H, G, d):
+    """o, lse and the workspace lie between bytes that stay as they are, and every value is set."""
+    rng = np.random.default_rng(B)
+    c = filled(rng.integers(0, 90, B).tolist() + [2000], 16, H, d, dtype, seed=90)
+    B += 1
+    dev, q = Dev(c), queries(B, H * G, d, dtype, 90)
+    need = lib().gret_paged_attention_workspace_size(dtype, H * G, H, d)
+    sizes = [q.numel() * q.element_size(), 4 * B * H * G, need]
+    bufs = [torch.full((n + 512,), 0x7b, dtype=torch.uint8, device="cuda") for n in sizes]
+    o, lse, ws = (b[256:256 + n] for b, n in zip(bufs, sizes))
+    o, lse = o.view(dtype).view(q.shape), lse.view(torch.float32).view(B, H * G)
+    lib().gret_paged_attention_decode(q, dev.lens, dev.table, dev.k, dev.v, o=o, lse=lse,
+                                      workspace=ws)
+    check(c, q, o, lse)
+    for b, n in zip(bufs, sizes):
+        assert (b[:256] == 0x7b).all() and (b[256 + n:] == 0x7b).all()
