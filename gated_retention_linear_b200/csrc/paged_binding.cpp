@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -142,19 +143,23 @@ struct Pool {
     }
 };
 
+// A given workspace, or one of the call's own: memory of torch's allocator for the current stream,
+// without a tensor around it.
 struct Workspace {
-    at::Tensor own;
+    c10::DataPtr own;
     void* at;
     size_t bytes;
 
-    Workspace(const at::Tensor* given, size_t need, const at::Tensor& like) {
-        if (given && !given->is_contiguous())
-            refuse(PyExc_ValueError, "workspace must be contiguous");
-        if (!given)
-            own = at::empty({(int64_t)(need > 16 ? need : 16)}, like.options().dtype(at::kByte));
-        const at::Tensor& t = given ? *given : own;
-        at = t.data_ptr();
-        bytes = t.nbytes();
+    Workspace(const at::Tensor* given, size_t need) {
+        if (given) {
+            if (!given->is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+            at = given->data_ptr();
+            bytes = given->nbytes();
+        } else {
+            bytes = need > 16 ? need : 16;
+            own = c10::cuda::CUDACachingAllocator::get()->allocate(bytes);
+            at = own.get();
+        }
     }
 };
 
@@ -202,7 +207,7 @@ PyObject* attention_decode(PyObject* const* a) {
     at::Tensor lse;
     if (given_lse) lse = *given_lse;
     else if (a[9] == Py_True) lse = at::empty({B, Hq}, q.options().dtype(at::kFloat));
-    const Workspace w(ws, gret_paged_attention_workspace_size(p.dtype, Hq, p.H, p.d), q);
+    const Workspace w(ws, gret_paged_attention_workspace_size(p.dtype, Hq, p.H, p.d));
     check("gret_paged_attention_decode",
           gret_paged_attention_decode(
               q.data_ptr(), lens_at, table.entries, table.stride, table.max_pages, p.k, p.v, p.sp,
@@ -251,7 +256,7 @@ PyObject* resize(PyObject* const* a) {
     const Table table(pt, S);
     const Scope scope(a[10], lens, {&delta, &pt, &ref, &kp, &vp, given, status, ws});
     const at::Tensor pos = int32_output(given, S, lens);
-    const Workspace w(ws, gret_paged_resize_workspace_size(S), lens);
+    const Workspace w(ws, gret_paged_resize_workspace_size(S));
     check("gret_paged_resize",
           gret_paged_resize(int32s(&delta, "delta", S), int32s(&lens, "seq_lens", S), S,
                             table.entries, table.stride, table.max_pages,
@@ -292,7 +297,7 @@ PyObject* compact(PyObject* const* a) {
     const Table table(pt, S);
     const Scope scope(a[9], lens, {&pt, &ref, &kp, &vp, given, status, ws});
     const at::Tensor n_live = int32_output(given, 1, lens);
-    const Workspace w(ws, gret_paged_compact_workspace_size(p.n_pages), lens);
+    const Workspace w(ws, gret_paged_compact_workspace_size(p.n_pages));
     check("gret_paged_compact",
           gret_paged_compact(int32s(&lens, "seq_lens", S), S, table.entries, table.stride,
                              table.max_pages, int32s(&ref, "ref", p.n_pages), p.k, p.v, p.sp, p.st,
