@@ -53,13 +53,11 @@ constexpr int NW = NT / 32;
 constexpr int UNIT = 32;               // keys of one unit of work
 constexpr int SHORT_TILES = 8;         // pairs of up to so many are worked on by single warps,
 constexpr int MIN_SHORT = 592;         // where there are at least so many of them
-constexpr int S = 3;                   // tiles of a warp's ring
 constexpr int HALF = 4096;             // bytes of a tile's keys, and of its values
-constexpr int RING = S * 2 * HALF;
+constexpr int STAGE = 2 * HALF;
 constexpr int MAXROWS_BF16 = 24;       // query rows a block works on at a time: what registers hold
 constexpr int MAXROWS_F32 = 16;
-constexpr int BLOCKS_SM = 2;           // 2 x (4 rings of 24 KB + queries) fill an SM's 227 KB
-constexpr int GRID = 148 * BLOCKS_SM;
+constexpr int MAX_GRID = 148 * 3;
 constexpr int JOIN_Y = 8;              // blocks a pair of the join: 8 x GRID are in place at once
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -158,6 +156,7 @@ struct Bf16Math {
     static constexpr int QROW = ROWB + 16;           // 16 more bytes: rows begin in other banks
     static constexpr int QBYTES = ROWS * QROW, SCRATCH = 0, NPASS = NQ;
     static constexpr bool BY_WARPS = false, SPARE = ROWS * D <= 1536;   // see ByWarps
+    static constexpr int S = 3, BLOCKS = 2;          // stages of a warp's ring, blocks an SM
 
     // The queries' fragments stay in registers where these suffice; 24 rows of 128 would take 48 on
     // top of the sums' 96, and are read from shared memory for every 16 keys.
@@ -328,6 +327,10 @@ struct F32Math {
     static constexpr int QROW = D / 32 * 144;
     static constexpr int QBYTES = R * QROW, SCRATCH = KT * R * 4, NPASS = 1;
     static constexpr bool BY_WARPS = false, SPARE = R * D <= 1024;
+    // Three blocks an SM with a tile less each, where latency of the arithmetic bounds the kernel and
+    // 168 registers do (8 rows of 128: 104 -> 98 us; 12 rows, with them spilled, 284 -> 327).
+    static constexpr bool MORE = R == 8 && D == 128;
+    static constexpr int S = MORE ? 2 : 3, BLOCKS = MORE ? 3 : 2;
 
     float m[R], l[R];
     float2 acc[R][2];            // dimensions 4 (lane % CPR) and on
@@ -457,7 +460,8 @@ struct F32Math {
 template <class M>
 struct ByWarps : M {
     static constexpr bool BY_WARPS = true;
-    static_assert(M::QBYTES <= 2 * HALF, "a stage of the ring holds the queries");
+    static constexpr int S = 3, BLOCKS = 2;
+    static_assert(M::QBYTES <= STAGE, "a stage of the ring holds the queries");
 };
 
 // Keys [first, len) of sequence b.
@@ -486,7 +490,7 @@ __device__ __forceinline__ int units_of(const Params& p, int b) {
 // a us.
 template <class M>
 constexpr int end_units() {
-    constexpr int unit_ns = UNIT * 2 * M::ROWB * 1000 / 22000, end_ns = 300 + 1200 * M::NPASS;
+    constexpr int unit_ns = UNIT * 2 * M::ROWB * M::BLOCKS / 44, end_ns = 300 + 1200 * M::NPASS;
     return (end_ns + unit_ns / 2) / unit_ns < 1 ? 1 : (end_ns + unit_ns / 2) / unit_ns;
 }
 
@@ -665,7 +669,7 @@ __device__ __forceinline__ Share share_of(const Params& p, DealSmem& sm) {
             shorts_all = 0;
         }
     }
-    Share r = {Deal(longs_all, GRID), Deal(shorts_all, GRID * NW), -1, -1, 0, 0,
+    Share r = {Deal(longs_all, 148 * M::BLOCKS), Deal(shorts_all, 148 * M::BLOCKS * NW), -1, -1, 0, 0,
                by_warps ? LONG : ANY};
     // the thread that holds the first unit of a share says where it is
     auto find = [&](int64_t u, int64_t at, int64_t mine, bool want, int slot) {
@@ -705,7 +709,7 @@ __device__ __forceinline__ Share share_of(const Params& p, DealSmem& sm) {
 // tiles.
 template <class M>
 struct Loader {
-    static constexpr int KT = M::KT, ROWB = M::ROWB, CPR = ROWB / 16;
+    static constexpr int KT = M::KT, ROWB = M::ROWB, CPR = ROWB / 16, S = M::S;
 
     struct Tile {
         int64_t head;            // bytes from a slot to its head's row
@@ -793,7 +797,7 @@ __device__ __forceinline__ void work_by_warp(const Params& p, M& math, const Sha
                                              unsigned char* ring, unsigned char* scratch, float* wm,
                                              float* wl) {
     using T = typename M::T;
-    constexpr int D = M::D, CPR = M::ROWB / 16, STAGE = 2 * HALF;
+    constexpr int D = M::D, CPR = M::ROWB / 16;
     constexpr int PR = M::ROWS / M::NPASS, FIT = STAGE / (PR * D * 4);
     const int lane = threadIdx.x & 31, worker = blockIdx.x * NW + (threadIdx.x >> 5);
     const int64_t u1 = share.shorts.begin(worker + 1);
@@ -848,9 +852,9 @@ __device__ __forceinline__ void work_by_warp(const Params& p, M& math, const Sha
 }
 
 template <class M>
-__global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params p) {
+__global__ void __launch_bounds__(NT, M::BLOCKS) paged_attn_kernel(const Params p) {
     using T = typename M::T;
-    constexpr int D = M::D, KT = M::KT, CPR = M::ROWB / 16;
+    constexpr int D = M::D, KT = M::KT, CPR = M::ROWB / 16, S = M::S, RING = S * STAGE;
     constexpr int QC = (M::ROWS * CPR + NT - 1) / NT;      // pieces of the queries a thread moves
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float wm[NW][M::ROWS], wl[NW][M::ROWS];
@@ -902,7 +906,7 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
     Loader<M> loader(p, seg, share.kind, u1, warp * KT, NW * KT, lane);
     unsigned ok[S];
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) ok[i] = loader.load(p, ring + i * 2 * HALF, lane);
+    for (int i = 0; i < S - 1; ++i) ok[i] = loader.load(p, ring + i * STAGE, lane);
     int stage = 0;
     put_q();
     __syncthreads();
@@ -914,10 +918,10 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         math.begin(qs, lane);
         const uint32_t key1 = seg.key1();
         for (uint32_t k = seg.key0() + warp * KT; k < key1; k += NW * KT) {
-            ok[S - 1] = loader.load(p, ring + (stage == 0 ? S - 1 : stage - 1) * 2 * HALF, lane);
+            ok[S - 1] = loader.load(p, ring + (stage == 0 ? S - 1 : stage - 1) * STAGE, lane);
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
             __syncwarp();
-            const unsigned char* t = ring + stage * 2 * HALF;
+            const unsigned char* t = ring + stage * STAGE;
             math.tile(t, t + HALF, qs, scratch, ok[0], p.scale_log2, lane);
             __syncwarp();
 #pragma unroll
@@ -935,11 +939,11 @@ __global__ void __launch_bounds__(NT, BLOCKS_SM) paged_attn_kernel(const Params 
         // in passes of as many rows as the stage holds; when the block ends here, nothing is under
         // way, and one pass does
         constexpr int PR = M::ROWS / M::NPASS;             // rows of a tile of queries
-        constexpr int FIT = 2 * HALF / (PR * D * 4) < M::NPASS ? 2 * HALF / (PR * D * 4) : M::NPASS;
+        constexpr int FIT = STAGE / (PR * D * 4) < M::NPASS ? STAGE / (PR * D * 4) : M::NPASS;
         static_assert(M::ROWS * D * 4 <= RING && FIT >= 1, "");
         const int np = go ? FIT : M::NPASS;
         float* mine_put = reinterpret_cast<float*>(
-            ring + (go ? (stage == 0 ? S - 1 : stage - 1) * 2 * HALF : 0));
+            ring + (go ? (stage == 0 ? S - 1 : stage - 1) * STAGE : 0));
         if (lane == 0) wput[warp] = mine_put;
         math.end(wm[warp], wl[warp], lane);
 #pragma unroll 1
@@ -989,7 +993,7 @@ template <class M>
 __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M::D>* parts, int n,
                                          int r, int64_t head) {
     using T = typename M::T;
-    constexpr int D = M::D, E = D / 32, UN = 8, PER = (GRID + NT - 1) / NT;
+    constexpr int D = M::D, E = D / 32, UN = 8, GRID = 148 * M::BLOCKS, PER = (GRID + NT - 1) / NT;
     __shared__ float w[GRID];                              // the parts' weights
     __shared__ float sums[NW][D], red[2][NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1064,7 +1068,7 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
     constexpr int D = M::D;
     const int tid = threadIdx.x, c = blockIdx.x;
     // sequences without keys: zeros, with nothing to wait for
-    for (int b = c; b < p.table.S; b += GRID)
+    for (int b = c; b < p.table.S; b += 148 * M::BLOCKS)
         if (units_of(p, b) == 0)
             for (int i = blockIdx.y; i < p.Hq; i += gridDim.y) {
                 for (int e = tid; e < D; e += NT)
@@ -1082,23 +1086,24 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
 }
 
 template <class M>
-cudaError_t launch(Params& p, cudaStream_t stream) {
-    constexpr int smem = NW * (RING + M::SCRATCH) + M::QBYTES;
-    p.QG = (p.G + M::ROWS - 1) / M::ROWS;
-    cudaError_t e;
-    if (M::SPARE && (int64_t)p.table.S * p.pool.H * p.QG >= MIN_SHORT) {
-        using W = typename std::conditional<M::SPARE, ByWarps<M>, M>::type;
-        e = allow_smem<paged_attn_kernel<W>>(smem, smem);
-        if (e == cudaSuccess)
-            e = launch_early(paged_attn_kernel<W>, dim3(GRID), NT, smem, stream, p);
-    } else {
-        e = allow_smem<paged_attn_kernel<M>>(smem, smem);
-        if (e == cudaSuccess)
-            e = launch_early(paged_attn_kernel<M>, dim3(GRID), NT, smem, stream, p);
-    }
+cudaError_t launch_form(const Params& p, cudaStream_t stream) {
+    constexpr int grid = 148 * M::BLOCKS;
+    constexpr int smem = NW * (M::S * STAGE + M::SCRATCH) + M::QBYTES;
+    static_assert(M::BLOCKS * (smem + 3072) <= 228 * 1024 && grid <= MAX_GRID, "");
+    cudaError_t e = allow_smem<paged_attn_kernel<M>>(smem, smem);
     if (e != cudaSuccess) return e;
-    return launch_early(paged_join_kernel<M>, dim3(GRID, p.G < JOIN_Y ? p.G : JOIN_Y), NT, 0,
-                        stream, p);
+    e = launch_early(paged_attn_kernel<M>, dim3(grid), NT, smem, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_early(paged_join_kernel<M>, dim3(grid, p.G < JOIN_Y ? p.G : JOIN_Y), NT, 0, stream,
+                        p);
+}
+
+template <class M>
+cudaError_t launch(Params& p, cudaStream_t stream) {
+    p.QG = (p.G + M::ROWS - 1) / M::ROWS;
+    using W = typename std::conditional<M::SPARE, ByWarps<M>, M>::type;
+    return (int64_t)p.table.S * p.pool.H * p.QG >= MIN_SHORT ? launch_form<W>(p, stream)
+                                                             : launch_form<M>(p, stream);
 }
 
 // Query rows a block works on at a time: all G heads of a group where they fit, else the fewest
@@ -1128,8 +1133,8 @@ cudaError_t launch_d(bool bf16, int rows, Params& p, cudaStream_t stream) {
 }  // namespace
 
 size_t paged_attn_workspace(bool bf16, int Hq, int Hkv, int d) {
-    const size_t head = (GRID * sizeof(Header) + 255) / 256 * 256;
-    return head + (size_t)2 * GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
+    const size_t head = (MAX_GRID * sizeof(Header) + 255) / 256 * 256;
+    return head + (size_t)2 * MAX_GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
@@ -1146,7 +1151,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.lse = a.lse;
     p.status = a.status;
     p.headers = static_cast<Header*>(a.workspace);
-    p.parts = static_cast<unsigned char*>(a.workspace) + (GRID * sizeof(Header) + 255) / 256 * 256;
+    p.parts = static_cast<unsigned char*>(a.workspace) + (MAX_GRID * sizeof(Header) + 255) / 256 * 256;
     const int rows = rows_of(a.bf16, p.G);
     return a.d == 64 ? launch_d<64>(a.bf16, rows, p, stream)
                      : launch_d<128>(a.bf16, rows, p, stream);
