@@ -225,29 +225,28 @@ struct Bf16Math {
             const bool ok0 = ok >> (j + lane / 4) & 1, ok1 = ok >> (j + 8 + lane / 4) & 1;
             uint32_t hi[NQ][2], lo[NQ][2];
             bool up = false;
-            float mn[NQ][2];
 #pragma unroll
             for (int i = 0; i < NQ; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     s[i][e] = ok0 ? s[i][e] * scale : -INFINITY;
                     s[i][2 + e] = ok1 ? s[i][2 + e] * scale : -INFINITY;
-                    float x = fmaxf(s[i][e], s[i][2 + e]);
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-                    mn[i][e] = fmaxf(m[i][e], x);
-                    up |= mn[i][e] != m[i][e];
+                    up |= s[i][e] > m[i][e] || s[i][2 + e] > m[i][e];
                 }
+            // the maxima rise ever more seldom: the lanes compare theirs only where one does
             if (__any_sync(~0u, up)) {
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(m[i][e], fmaxf(s[i][e], s[i][2 + e]));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
                         // m = -inf: nothing summed up so far, whatever the factor
-                        f[e] = m[i][e] == -INFINITY ? 0.f : ex2(m[i][e] - mn[i][e]);
+                        f[e] = m[i][e] == -INFINITY ? 0.f : ex2(m[i][e] - x);
                         l[i][e] *= f[e];
-                        m[i][e] = mn[i][e];
+                        m[i][e] = x;
                     }
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
@@ -369,7 +368,6 @@ struct F32Math {
             }
         }
         const bool okk = ok >> key & 1;
-        float mn[R];
         bool up = false;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -377,18 +375,17 @@ struct F32Math {
 #pragma unroll
             for (int o = KT; o < 32; o <<= 1) s[r] += __shfl_xor_sync(~0u, s[r], o);
             s[r] = okk ? s[r] * scale : -INFINITY;
-            float x = s[r];
-#pragma unroll
-            for (int o = 1; o < KT; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-            mn[r] = fmaxf(m[r], x);
-            up |= mn[r] != m[r];
+            up |= s[r] > m[r];
         }
-        if (__any_sync(~0u, up)) {
+        if (__any_sync(~0u, up)) {             // as for bf16
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - mn[r]);
+                float x = fmaxf(m[r], s[r]);
+#pragma unroll
+                for (int o = 1; o < KT; o <<= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+                const float f = m[r] == -INFINITY ? 0.f : ex2(m[r] - x);
                 l[r] *= f;
-                m[r] = mn[r];
+                m[r] = x;
                 acc[r][0] = sm100::mul2(acc[r][0], make_float2(f, f));
                 acc[r][1] = sm100::mul2(acc[r][1], make_float2(f, f));
             }
