@@ -4,7 +4,7 @@
 // Which pages are free is ref[p] == 0, nothing else: no free list to keep in step.  A call that
 // takes pages takes the lowest free ones, row after row, so the outcome depends on the inputs
 // alone.  Finding them is a ranking of the free pages (how many free pages lie below p), which a
-// cluster of CL blocks does in one launch: ref is cut into up to MAXCH chunks, warps count the
+// cluster of 8 or 16 blocks does in one launch: ref is cut into up to MAXCH chunks, warps count the
 // free pages of theirs and leave the counts in every block's shared memory (distributed shared
 // memory), each block sums them up, and the chunks that hold pages to hand out are dealt over the
 // cluster's warps once more.  What is to be done to keys, values and tables follows in a second
@@ -23,7 +23,9 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int CL = 8;                  // blocks of a planning cluster (the portable maximum)
+constexpr int CL_FEW = 8;              // blocks of a planning cluster: the portable maximum,
+constexpr int CL_MANY = 16;            // and what the GPU allows, for pools of
+constexpr int MANY_PAGES = 1 << 18;    // so many pages
 constexpr int PNT = 1024;
 constexpr int PNW = PNT / 32;
 constexpr int MAXCH = 4 * PNT;         // chunks of ref
@@ -132,29 +134,36 @@ __device__ __forceinline__ int4 ranks_of(int4 q, int& before) {
 // Counts each chunk's free pages into `count` [MAXCH] of every block of the cluster.  Starts with
 // the second half of a cluster barrier (whoever calls has arrived) and ends with a whole one: what
 // the cluster's blocks read of the inputs beforehand, no block changes before that.
+template <int CL>
 __device__ __forceinline__ void count_free(const Chunks& ch, int* count) {
     cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = cluster.block_rank() * PNW + (threadIdx.x >> 5);
     bool begun = false;
     for (int c0 = warp; c0 < ch.n; c0 += CL * PNW * GROUP) {
         int n[GROUP] = {};
-        const int far = CL * PNW * ch.step, first = c0 * ch.step;
-        if (ch.inside(first) && (int64_t)first + (GROUP - 1) * (int64_t)far + ch.step <= ch.P / 4) {
-            // plain loads, so that all of them are on their way before the first is looked at
+        bool whole[GROUP];                       // chunks that lie in ref with all their quads
+#pragma unroll
+        for (int g = 0; g < GROUP; ++g) {
+            const int c = c0 + g * CL * PNW;
+            whole[g] = c < ch.n && ch.inside(c * ch.step) && ch.inside((c + 1) * ch.step - 1);
+        }
+        // all loads of an iteration are on their way before the first is looked at
 #pragma unroll 2
-            for (int i = lane; i < ch.step; i += 32) {
-                int4 x[GROUP];
+        for (int i = lane; i < ch.step; i += 32) {
+            int4 x[GROUP];
 #pragma unroll
-                for (int g = 0; g < GROUP; ++g) x[g] = ch.inner_quad(first + g * far + i);
-#pragma unroll
-                for (int g = 0; g < GROUP; ++g) n[g] += free_of(x[g]);
+            for (int g = 0; g < GROUP; ++g) {
+                x[g] = make_int4(1, 1, 1, 1);
+                if (whole[g]) x[g] = ch.inner_quad((c0 + g * CL * PNW) * ch.step + i);
             }
-        } else {
 #pragma unroll
-            for (int g = 0; g < GROUP; ++g)
-                if (c0 + g * CL * PNW < ch.n)
-                    for (int i = lane; i < ch.step; i += 32)
-                        n[g] += free_of(ch.quad(first + g * far + i));
+            for (int g = 0; g < GROUP; ++g) n[g] += free_of(x[g]);
+        }
+#pragma unroll
+        for (int g = 0; g < GROUP; ++g) {
+            const int c = c0 + g * CL * PNW;
+            if (c < ch.n && !whole[g])
+                for (int i = lane; i < ch.step; i += 32) n[g] += free_of(ch.quad(c * ch.step + i));
         }
         if (!begun) cluster.barrier_wait();      // every block runs: its shared memory is there
         begun = true;
@@ -237,6 +246,39 @@ __device__ __forceinline__ void copy_pieces(const PagedPool& p, const Pieces& pc
         *reinterpret_cast<uint4*>(p.k + to * p.sp + off) = k;
         *reinterpret_cast<uint4*>(p.v + to * p.sp + off) = v;
     }
+}
+
+// Whether the current device places clusters of CL_MANY blocks of a planning kernel with up to `smem`
+// bytes, asked once on each of the first 64 devices.
+template <auto Kernel>
+bool many_blocks(int smem) {
+    static std::atomic<uint64_t> asked{0}, fits{0};
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || device >= 64) return false;
+    const uint64_t bit = (uint64_t)1 << device;
+    if (!(asked.load(std::memory_order_acquire) & bit)) {
+        cudaLaunchAttribute dims;
+        dims.id = cudaLaunchAttributeClusterDimension;
+        dims.val.clusterDim.x = CL_MANY;
+        dims.val.clusterDim.y = dims.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(CL_MANY);
+        cfg.blockDim = dim3(PNT);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &dims;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool ok =
+            cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+                cudaSuccess &&
+            cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+                cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) == cudaSuccess && n > 0;
+        cudaGetLastError();      // an answer of no leaves no error behind
+        if (ok) fits.fetch_or(bit, std::memory_order_release);
+        asked.fetch_or(bit, std::memory_order_release);
+    }
+    return fits.load(std::memory_order_acquire) & bit;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -327,8 +369,6 @@ __global__ void __launch_bounds__(NT) append_kernel(const PagedAppendArgs a, con
 // of 1000 rows that come and go on 786433 pages (25 us) counting takes 6, 50 GB/s an SM, handing out
 // 6.
 
-constexpr int ROWS_U = 4;              // rows that a planning thread looks at at once
-
 // A row's change, from its length before the call.
 struct Change {
     int64_t n0, n1;
@@ -342,6 +382,60 @@ __device__ __forceinline__ Change change_of(const PagedResizeArgs& a, int s) {
     if (c.n1 < 0) c.n1 = 0;
     c.bad = c.n0 < 0 || c.n0 > (int64_t)a.table.max_pages << a.pool.page_shift;
     return c;
+}
+
+// What the rows [s0, s1) ask for: pages in all, each row's to upto, the table entry that the first goes
+// to, and where `lead` the plan in workspace and pos.
+template <int U>
+__device__ __forceinline__ int64_t needs_of(const PagedResizeArgs& a, int s0, int s1, bool lead,
+                                            int* upto, int* first) {
+    const int shift = a.pool.page_shift;
+    int64_t mine = 0;
+    for (int sb = s0; sb < s1; sb += U) {
+        // length, last page, its count: three loads one after another, of U rows side by side
+        Change c[U];
+        int id[U], count[U];
+        bool fits[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            c[u] = {0, 0, false};
+            if (sb + u < s1) c[u] = change_of(a, sb + u);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            fits[u] = !c[u].bad && c[u].n1 > c[u].n0 &&
+                      c[u].n1 <= (int64_t)a.table.max_pages << shift;
+            id[u] = -1;
+            if (fits[u] && (c[u].n0 & ((1 << shift) - 1))) {
+                id[u] = a.table.entries[(sb + u) * a.table.stride + (c[u].n0 >> shift)];
+                if ((unsigned)id[u] >= (unsigned)a.pool.n_pages) {
+                    if (lead) paged_flag(a.status, GRET_PAGED_BAD_PAGE);
+                    id[u] = -1;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) count[u] = id[u] >= 0 ? a.ref[id[u]] : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = sb + u;
+            if (s >= s1) break;
+            if (lead && c[u].bad) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
+            if (lead && !c[u].bad && c[u].n1 > c[u].n0 && !fits[u])
+                paged_flag(a.status, GRET_PAGED_TABLE_FULL);
+            const int c0 = pages_of(c[u].n0, shift), c1 = pages_of(c[u].n1, shift);
+            const bool copies = count[u] > 1;
+            const int need = fits[u] ? c1 - c0 + copies : 0;
+            upto[s] = need;
+            first[s] = fits[u] ? c0 - copies : 0;
+            if (lead) {
+                a.workspace[s] = copies ? id[u] : -1;
+                a.pos[s] = fits[u] ? (int)c[u].n0 : -1;
+            }
+            mine += need;
+        }
+    }
+    return mine;
 }
 
 // The first of S rows with upto > rank (there is one), by a whole warp.
@@ -360,6 +454,7 @@ __device__ __forceinline__ int row_of_rank(const int* upto, int S, int rank) {
 
 // Leaves pos, the new pages' ref and table entries, and in workspace[s] the page that row s is to
 // copy its last, partly filled one from (-1: none).
+template <int CL>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT, 1)
     resize_plan_kernel(const PagedResizeArgs a) {
     extern __shared__ int rows_smem[];
@@ -378,53 +473,10 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT, 1)
     // every block works out all rows' needs; the first one writes the plan
     const int per = (S + PNT - 1) / PNT;
     const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
-    int64_t mine = 0;
-    for (int sb = s0; sb < s1; sb += ROWS_U) {
-        // length, last page, its count: three loads one after another, of ROWS_U rows side by side
-        Change c[ROWS_U];
-        int id[ROWS_U], count[ROWS_U];
-        bool fits[ROWS_U];
-#pragma unroll
-        for (int u = 0; u < ROWS_U; ++u) {
-            c[u] = {0, 0, false};
-            if (sb + u < s1) c[u] = change_of(a, sb + u);
-        }
-#pragma unroll
-        for (int u = 0; u < ROWS_U; ++u) {
-            fits[u] = !c[u].bad && c[u].n1 > c[u].n0 &&
-                      c[u].n1 <= (int64_t)a.table.max_pages << shift;
-            id[u] = -1;
-            if (fits[u] && (c[u].n0 & ((1 << shift) - 1))) {
-                id[u] = a.table.entries[(sb + u) * a.table.stride + (c[u].n0 >> shift)];
-                if ((unsigned)id[u] >= (unsigned)a.pool.n_pages) {
-                    if (lead) paged_flag(a.status, GRET_PAGED_BAD_PAGE);
-                    id[u] = -1;
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < ROWS_U; ++u) count[u] = id[u] >= 0 ? a.ref[id[u]] : 0;
-#pragma unroll
-        for (int u = 0; u < ROWS_U; ++u) {
-            const int s = sb + u;
-            if (s >= s1) break;
-            if (lead && c[u].bad) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
-            if (lead && !c[u].bad && c[u].n1 > c[u].n0 && !fits[u])
-                paged_flag(a.status, GRET_PAGED_TABLE_FULL);
-            const int c0 = pages_of(c[u].n0, shift), c1 = pages_of(c[u].n1, shift);
-            const bool copies = count[u] > 1;
-            const int need = fits[u] ? c1 - c0 + copies : 0;
-            upto[s] = need;
-            first[s] = fits[u] ? c0 - copies : 0;
-            if (lead) {
-                a.workspace[s] = copies ? id[u] : -1;
-                a.pos[s] = fits[u] ? (int)c[u].n0 : -1;
-            }
-            mine += need;
-        }
-    }
+    const int64_t mine = per == 1 ? needs_of<1>(a, s0, s1, lead, upto, first)
+                                  : needs_of<4>(a, s0, s1, lead, upto, first);
     const Chunks ch(a.ref, a.pool.n_pages);
-    count_free(ch, chunk_before);
+    count_free<CL>(ch, chunk_before);
     int64_t run = mine;
     const int total = rank_free(ch, chunk_before, sums, run);
     for (int s = s0; s < s1; ++s) {
@@ -694,6 +746,7 @@ __host__ __device__ __forceinline__ CompactPlan compact_plan(const PagedCompactA
     return {a.workspace, a.workspace + 4, a.workspace + 4 + P, a.workspace + 4 + 2 * P};
 }
 
+template <int CL>
 __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT, 1)
     compact_plan_kernel(const PagedCompactArgs a) {
     __shared__ int64_t sums[PNW][2];
@@ -705,7 +758,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT, 1)
     const int lane = threadIdx.x & 31, P = a.pool.n_pages;
     const CompactPlan plan = compact_plan(a);
     const Chunks ch(a.ref, P);
-    count_free(ch, chunk_before);
+    count_free<CL>(ch, chunk_before);
     int64_t none = 0;
     const int L = P - rank_free(ch, chunk_before, sums, none);
     __syncthreads();
@@ -797,9 +850,15 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_paged_resize(const PagedResizeArgs& a, cudaStream_t stream) {
     const size_t smem = (size_t)a.table.S * 2 * sizeof(int);
-    cudaError_t e = allow_smem<resize_plan_kernel>(smem, PAGED_MAX_SEQS * 2 * (int)sizeof(int));
-    if (e != cudaSuccess) return e;
-    e = launch_early(resize_plan_kernel, dim3(CL), PNT, smem, stream, a);
+    constexpr int most_smem = PAGED_MAX_SEQS * 2 * (int)sizeof(int);
+    cudaError_t e;
+    if (a.pool.n_pages >= MANY_PAGES && many_blocks<resize_plan_kernel<CL_MANY>>(most_smem)) {
+        e = launch_early(resize_plan_kernel<CL_MANY>, dim3(CL_MANY), PNT, smem, stream, a);
+    } else {
+        e = allow_smem<resize_plan_kernel<CL_FEW>>(smem, most_smem);
+        if (e == cudaSuccess)
+            e = launch_early(resize_plan_kernel<CL_FEW>, dim3(CL_FEW), PNT, smem, stream, a);
+    }
     if (e != cudaSuccess) return e;
     return launch_early(resize_apply_kernel, dim3(APPLY_SM * 148), NT, 0, stream, a,
                         Pieces(a.pool));
@@ -831,7 +890,7 @@ cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_compact(const PagedCompactArgs& a, cudaStream_t stream) {
-    const cudaError_t e = launch_early(compact_plan_kernel, dim3(CL), PNT, 0, stream, a);
+    const cudaError_t e = launch_early(compact_plan_kernel<CL_FEW>, dim3(CL_FEW), PNT, 0, stream, a);
     if (e != cudaSuccess) return e;
     return launch_early(compact_move_kernel, dim3(GRID), NT, 0, stream, a, Pieces(a.pool));
 }
