@@ -25,8 +25,9 @@
 // ldmatrix, the accumulators stay in registers.  From 16 heads a group on the products and the
 // softmax no longer hide behind the loads: 24 heads on one kv head run at 0.58 of the copy
 // bandwidth, 12 of 128 at 0.88.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
-// the scores and a lane four dimensions for the values; 0.94 of the copy bandwidth at G = 3, 0.79 at
-// 8; at 16 (0.45) the queries' reads from shared memory bound it.
+// the scores and a lane four dimensions for the values; 0.94 of the copy bandwidth at G = 3, 0.85 at
+// 8; at 16 (0.46) the queries' reads from shared memory bound it.  16-bit heads of 64 in token-major
+// pages are 128-byte pieces, which HBM serves at 0.84 of the copy bandwidth (head-major: 0.97).
 //
 // The work is cut into units of UNIT keys of one (sequence, kv head, group of query rows), a pair;
 // the units of the whole batch are dealt out evenly over the grid, in order, so that one long

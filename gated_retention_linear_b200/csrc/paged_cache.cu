@@ -25,7 +25,8 @@ namespace {
 
 constexpr int CL_FEW = 8;              // blocks of a planning cluster: the portable maximum,
 constexpr int CL_MANY = 16;            // and what the GPU allows, for pools of
-constexpr int MANY_PAGES = 1 << 18;    // so many pages
+constexpr int MANY_PAGES = 1 << 17;    // so many pages (131072 of them, 1000 rows that come and go:
+                                       // 21.3 -> 18.7 us; 30000 to 110000 pages 1 to 2 % slower)
 constexpr int PNT = 1024;
 constexpr int PNW = PNT / 32;
 constexpr int MAXCH = 4 * PNT;         // chunks of ref
@@ -364,10 +365,10 @@ __global__ void __launch_bounds__(NT) append_kernel(const PagedAppendArgs a, con
 
 // ---------------------------------------------------------------------------------------------
 // resize: a plan by one cluster (who gets which page), then the whole GPU carries it out.  Latency
-// bounds it: of a step of 256 rows on 20000 pages (10 us) the plan takes 7 (rows 1.5, counting 1.4,
+// bounds it: of a step of 256 rows on 20000 pages (9.5 us) the plan takes 7 (rows 1.5, counting 1.4,
 // the cluster's barrier and the sums 1.2, handing out 1.5, the launch the rest) and the copies 2.7;
-// of 1000 rows that come and go on 786433 pages (25 us) counting takes 6, 50 GB/s an SM, handing out
-// 6.
+// of 1000 rows that come and go on 786433 pages (24 us) counting takes 5.5 (it reads 0.8 TB/s, with
+// 8 blocks or 16: they share one GPC's way to the L2), handing out 6, and the rows' lists 4.
 
 // A row's change, from its length before the call.
 struct Change {
