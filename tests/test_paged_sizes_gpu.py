@@ -349,3 +349,66 @@ def test_attention_writes_its_outputs_only(dtype, B, H, G, d):
     check(c, q, o, lse)
     for b, n in zip(bufs, sizes):
         assert (b[:256] == 0x7b).all() and (b[256 + n:] == 0x7b).all()
+
+
+def test_two_streams_at_once():
+    """Decode attention of two caches on two streams, calls of both in flight together, each with its
+    own workspace: the outputs are those of one call at a time."""
+    G = lib()
+    rng = np.random.default_rng(91)
+    sets = []
+    for seed, (B, H, G_, d, dtype) in enumerate([(300, 4, 3, 128, BF16), (6, 2, 8, 64, F32)]):
+        c = filled(rng.integers(1, 120 if B > 99 else 3000, B).tolist(), 16, H, d, dtype, seed=seed)
+        dev, q = Dev(c), queries(B, H * G_, d, dtype, seed)
+        sets.append((dev, q, dev.decode(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(30):
+        for i, (dev, q, _, stream) in enumerate(sets):
+            outs[i].append(G.gret_paged_attention_decode(q, dev.lens, dev.table, dev.k, dev.v,
+                                                         lse=True, stream=stream))
+    torch.cuda.synchronize()
+    for (_, _, (o, lse), _), many in zip(sets, outs):
+        assert all(torch.equal(o, x) and torch.equal(lse, y) for x, y in many)
+
+
+@pytest.mark.parametrize("P", [500, 140000])
+def test_captured_upkeep(P):
+    """Resize, fork and compact captured once and replayed on a cache that comes, goes and runs full,
+    with the lists of what to do written between the replays."""
+    G = lib()
+    rng = np.random.default_rng(P)
+    S, page, W = 30, 4, 60 if P < 1000 else 5000
+    c = Cache(S, W, P, page, 1, 8, BF16, fill=0.0)
+    dev = Dev(c)
+    delta, pos, src, dst = (i32(np.zeros(n)) for n in (S, S, 4, 4))
+    n_live = i32([0])
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda")
+          for n in (G.gret_paged_resize_workspace_size(S), G.gret_paged_compact_workspace_size(P))]
+
+    def step():
+        G.gret_paged_resize(delta, dev.lens, dev.table, dev.ref, dev.k, dev.v, pos=pos,
+                            workspace=ws[0])
+        G.gret_paged_fork(src, dst, dev.lens, dev.table, dev.ref, page)
+        G.gret_paged_compact(dev.lens, dev.table, dev.ref, dev.k, dev.v, n_live=n_live,
+                             workspace=ws[1])
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()                                       # nothing to do: loads the kernels
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    big = 200 if P < 1000 else 15000
+    for _ in range(25):
+        d = np.where(rng.random(S) < 0.5, rng.integers(-big, big, S), 1)
+        s, t = rng.integers(0, S, 4), rng.integers(0, S, 4)
+        for x, y in ((delta, d), (src, s), (dst, t)):
+            x.copy_(i32(y))
+        graph.replay()
+        rpos, _ = c.resize(d)
+        c.fork(s.tolist(), t.tolist())
+        n = c.compact()
+        assert np.array_equal(pos.cpu().numpy(), rpos) and int(n_live) == n
+        dev.same_as(c)
