@@ -26,8 +26,7 @@
 // softmax no longer hide behind the loads: 24 heads on one kv head run at 0.58 of the copy
 // bandwidth, 12 of 128 at 0.88.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
 // the scores and a lane four dimensions for the values; 0.94 of the copy bandwidth at G = 3, 0.85 at
-// 8; at 16 (0.46) the queries' reads from shared memory bound it.  16-bit heads of 64 in token-major
-// pages are 128-byte pieces, which HBM serves at 0.84 of the copy bandwidth (head-major: 0.97).
+// 8; at 16 (0.46) the queries' reads from shared memory bound it.
 //
 // The work is cut into units of UNIT keys of one (sequence, kv head, group of query rows), a pair;
 // the units of the whole batch are dealt out evenly over the grid, in order, so that one long
@@ -73,9 +72,9 @@ struct Header {
 
 // Parts in the workspace: slot 2c is block c's head (the rest of a pair begun by an earlier
 // block), slot 2c + 1 its tail (a pair that a later block goes on with).
-template <int R, int D>
+template <int MR, int R, int D>
 struct Part {
-    float m[R], l[R];            // m in units of log2
+    float m[MR], l[MR];            // m in units of log2
     float a[R][D];
 };
 
@@ -150,10 +149,15 @@ __device__ __forceinline__ int put_place(int D, int r, int e) {
     return r * D + (e ^ ((r >> 1 & 3) << 3));
 }
 
-template <int D_, int NQ>
+// HEADS_ = 2: the rows of two neighbouring kv heads, next to one another in memory, are one row of D
+// dimensions (and the two one head for the dealing).  Every head has its own query rows, maxima and
+// sums; its scores take its half of a key's row, and its outputs its half of a value's.
+template <int D_, int NQ, int HEADS_ = 1>
 struct Bf16Math {
     using T = __nv_bfloat16;
     static constexpr int D = D_, ROWS = 8 * NQ, ROWB = D * 2, KT = HALF / ROWB;
+    static constexpr int HEADS = HEADS_, DH = D / HEADS, MROWS = ROWS * HEADS;
+    static constexpr int NI = NQ * HEADS, KH = DH / 16;    // tiles of scores; steps of a head's
     static constexpr int QROW = ROWB + 16;           // 16 more bytes: rows begin in other banks
     static constexpr int QBYTES = ROWS * QROW, SCRATCH = 0, NPASS = NQ;
     static constexpr bool BY_WARPS = false, SPARE = ROWS * D <= 1536;   // see ByWarps
@@ -164,7 +168,7 @@ struct Bf16Math {
     static constexpr bool KEEP_Q = NQ * D <= 256;
 
     uint32_t qf[KEEP_Q ? NQ : 1][D / 16][2];
-    float m[NQ][2], l[NQ][2], acc[NQ][D / 16][4];
+    float m[NI][2], l[NI][2], acc[NQ][D / 16][4];
 
     __device__ static __forceinline__ int q_place(int r, int c) { return r * QROW + c * 16; }
 
@@ -182,6 +186,9 @@ struct Bf16Math {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][k][e] = 0.f;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
             m[i][0] = m[i][1] = -INFINITY;
             l[i][0] = l[i][1] = 0.f;
         }
@@ -196,9 +203,9 @@ struct Bf16Math {
         const uint32_t qb = sm100::smem_u32(qs) + (lane & 7) * QROW + (lane >> 3) * 16;
 #pragma unroll
         for (int j = 0; j < KT; j += 16) {
-            float s[NQ][4];
+            float s[NI][4];                      // tile i: head i / NQ, query rows 8 (i % NQ) on
 #pragma unroll
-            for (int i = 0; i < NQ; ++i)
+            for (int i = 0; i < NI; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
 #pragma unroll
@@ -218,16 +225,16 @@ struct Bf16Math {
                     } else {
                         ldmatrix4(b, qb + 8 * i * QROW + 32 * k);
                     }
-                    mma_16x8x16(s[i], a[0], b[0], b[1]);
-                    mma_16x8x16(s[i], a[1], b[2], b[3]);
+                    mma_16x8x16(s[k / KH * NQ + i], a[0], b[0], b[1]);
+                    mma_16x8x16(s[k / KH * NQ + i], a[1], b[2], b[3]);
                 }
             }
-            // s[i]: key lane/4 (0, 1) and lane/4 + 8 (2, 3), queries 8i + 2 (lane & 3) and the next
+            // s[i]: key lane/4 (0, 1) and lane/4 + 8 (2, 3), queries 2 (lane & 3) and the next
             const bool ok0 = ok >> (j + lane / 4) & 1, ok1 = ok >> (j + 8 + lane / 4) & 1;
-            uint32_t hi[NQ][2], lo[NQ][2];
+            uint32_t hi[NI][2], lo[NI][2];
             bool up = false;
 #pragma unroll
-            for (int i = 0; i < NQ; ++i)
+            for (int i = 0; i < NI; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     s[i][e] = ok0 ? s[i][e] * scale : -INFINITY;
@@ -237,7 +244,7 @@ struct Bf16Math {
             // the maxima rise ever more seldom: the lanes compare theirs only where one does
             if (__any_sync(~0u, up)) {
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) {
+                for (int i = 0; i < NI; ++i) {
                     float f[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -250,13 +257,13 @@ struct Bf16Math {
                         m[i][e] = x;
                     }
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
+                    for (int k = 0; k < KH; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][k][e] *= f[e & 1];
+                        for (int e = 0; e < 4; ++e) acc[i % NQ][i / NQ * KH + k][e] *= f[e & 1];
                 }
             }
 #pragma unroll
-            for (int i = 0; i < NQ; ++i) {
+            for (int i = 0; i < NI; ++i) {
                 float p[4], x[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -282,17 +289,18 @@ struct Bf16Math {
                 ldmatrix4_trans(a, vb + r * ROWB + ((c ^ (r & 7)) << 4));
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
-                    mma_16x8x16(acc[i][k], a, hi[i][0], hi[i][1]);
-                    mma_16x8x16(acc[i][k], a, lo[i][0], lo[i][1]);
+                    const int h = k / KH * NQ + i;
+                    mma_16x8x16(acc[i][k], a, hi[h][0], hi[h][1]);
+                    mma_16x8x16(acc[i][k], a, lo[h][0], lo[h][1]);
                 }
             }
         }
     }
 
-    // The warp's maxima and sums of all rows.
+    // The warp's maxima and sums of all rows, head after head.
     __device__ __forceinline__ void end(float* wm, float* wl, int lane) {
 #pragma unroll
-        for (int i = 0; i < NQ; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -322,6 +330,7 @@ template <int D_, int R>
 struct F32Math {
     using T = float;
     static constexpr int D = D_, ROWS = R, ROWB = D * 4, KT = HALF / ROWB;
+    static constexpr int HEADS = 1, DH = D, MROWS = R;
     static constexpr int CPR = ROWB / 16, KI = 32 / CPR;   // pieces a row; rows a warp-wide read
     // a query row in parts of 32 dimensions, 16 bytes between them: the parts begin in other banks
     static constexpr int QROW = D / 32 * 144;
@@ -553,9 +562,9 @@ struct Segment {
         t1 = kind == SHORT ? nu : (int)min((int64_t)nu, u1 - u);
         return true;
     }
-    // Its queries: the first of them, and how many.
+    // Its queries: the first of them, and how many (of each of its heads, G further on).
     __device__ __forceinline__ int64_t head(const Params& p) const {
-        return (int64_t)b * p.Hq + pr / p.QG * p.G + pr % p.QG * M::ROWS;
+        return (int64_t)b * p.Hq + pr / p.QG * (M::HEADS * p.G) + pr % p.QG * M::ROWS;
     }
     __device__ __forceinline__ int rows(const Params& p) const {
         return min(M::ROWS, p.G - pr % p.QG * M::ROWS);
@@ -596,6 +605,9 @@ struct DealSmem {
     int64_t longs[NW], shorts[NW], unit[NW + 1];
     int n_short[NW], b[NW + 1];
 };
+
+template <class M>
+using PartOf = Part<M::MROWS, M::ROWS, M::D>;
 
 // What is dealt to a block and to this warp of it: units of long pairs and of short ones, the
 // sequence of the first of them, and that one's first unit.
@@ -778,14 +790,30 @@ struct Loader {
     }
 };
 
-// Four dimensions of an output row, and its lse from maximum (log2) and sum.
-template <typename T>
-__device__ __forceinline__ void put_out(const Params& p, int64_t head, int D, int e,
+// Of piece c of row r of the queries (and outputs) from `head` on: its place among all queries' pieces.
+template <class M>
+__device__ __forceinline__ int64_t query_piece(const Params& p, int64_t head, int r, int c) {
+    constexpr int PIECES = M::ROWB / 16 / M::HEADS;        // of a head's row
+    return (head + (M::HEADS == 1 ? 0 : c / PIECES * p.G) + r) * PIECES + c % PIECES;
+}
+
+// Where in a row's D dimensions e lies: the row of its maximum and sum.
+template <class M>
+__device__ __forceinline__ int max_row(int row, int e) {
+    return M::HEADS == 1 ? row : e / M::DH * M::ROWS + row;
+}
+
+// Four dimensions of row r of the outputs from `head` on, and the row's lse from maximum (log2) and
+// sum.
+template <class M>
+__device__ __forceinline__ void put_out(const Params& p, int64_t head, int r, int e,
                                         const float (&a)[4], float mx, float z) {
-    T* o = static_cast<T*>(p.o) + head * D + e;
+    using T = typename M::T;
+    const int64_t row = head + (M::HEADS == 1 ? 0 : e / M::DH * p.G) + r;
+    T* o = static_cast<T*>(p.o) + row * M::DH + e % M::DH;
 #pragma unroll
     for (int x = 0; x < 4; ++x) o[x] = from_f32<T>(a[x] / z);
-    if (p.lse && e == 0) p.lse[head] = (mx + log2f(z)) * LN2;
+    if (p.lse && e % M::DH == 0) p.lse[row] = (mx + log2f(z)) * LN2;
 }
 
 // The short pairs dealt to this warp, one after another, each from its first key to its output.  Two
@@ -794,7 +822,6 @@ template <class M>
 __device__ __forceinline__ void work_by_warp(const Params& p, M& math, const Share& share,
                                              unsigned char* ring, unsigned char* scratch, float* wm,
                                              float* wl) {
-    using T = typename M::T;
     constexpr int D = M::D, CPR = M::ROWB / 16;
     constexpr int PR = M::ROWS / M::NPASS, FIT = STAGE / (PR * D * 4);
     const int lane = threadIdx.x & 31, worker = blockIdx.x * NW + (threadIdx.x >> 5);
@@ -810,11 +837,12 @@ __device__ __forceinline__ void work_by_warp(const Params& p, M& math, const Sha
     for (bool go = true; go;) {
         const int rows = seg.rows(p);
         const int64_t head = seg.head(p);
-        const unsigned char* q =
-            static_cast<const unsigned char*>(p.q) + head * M::ROWB;
+        const uint4* q = static_cast<const uint4*>(p.q);
         for (int x = lane; x < M::ROWS * CPR; x += 32)
-            cp_async_16_or_zero(sm100::smem_u32(qs + M::q_place(x / CPR, x % CPR)),
-                                x < rows * CPR ? q + x * 16 : q, x < rows * CPR ? 16 : 0);
+            cp_async_16_or_zero(
+                sm100::smem_u32(qs + M::q_place(x / CPR, x % CPR)),
+                x < rows * CPR ? q + query_piece<M>(p, head, x / CPR, x % CPR) : q,
+                x < rows * CPR ? 16 : 0);
         asm volatile("cp.async.commit_group;" ::: "memory");
         const uint32_t key0 = seg.key0(), key1 = seg.key1();
         for (uint32_t k = key0; k < key1; k += M::KT) {
@@ -841,7 +869,8 @@ __device__ __forceinline__ void work_by_warp(const Params& p, M& math, const Sha
                 const int r = i / (D / 4), e = i % (D / 4) * 4;
                 const float4 x = *reinterpret_cast<const float4*>(buf + put_place(D, r, e));
                 const float a[4] = {x.x, x.y, x.z, x.w};
-                put_out<T>(p, head + row0 + r, D, e, a, wm[row0 + r], wl[row0 + r]);
+                put_out<M>(p, head, row0 + r, e, a, wm[max_row<M>(row0 + r, e)],
+                           wl[max_row<M>(row0 + r, e)]);
             }
             __syncwarp();
         }
@@ -851,11 +880,10 @@ __device__ __forceinline__ void work_by_warp(const Params& p, M& math, const Sha
 
 template <class M>
 __global__ void __launch_bounds__(NT, M::BLOCKS) paged_attn_kernel(const Params p) {
-    using T = typename M::T;
     constexpr int D = M::D, KT = M::KT, CPR = M::ROWB / 16, S = M::S, RING = S * STAGE;
     constexpr int QC = (M::ROWS * CPR + NT - 1) / NT;      // pieces of the queries a thread moves
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float wm[NW][M::ROWS], wl[NW][M::ROWS];
+    __shared__ float wm[NW][M::MROWS], wl[NW][M::MROWS];
     __shared__ const float* wput[NW];
     __shared__ DealSmem deal_smem;
     __shared__ Deal longs;
@@ -884,12 +912,13 @@ __global__ void __launch_bounds__(NT, M::BLOCKS) paged_attn_kernel(const Params 
     // A segment's queries: read one segment ahead, put into shared memory when it begins.
     uint4 qn[QC];
     auto read_q = [&](const Segment<M>& s) {
-        const T* q = static_cast<const T*>(p.q) + s.head(p) * D;
+        const uint4* q = static_cast<const uint4*>(p.q);
+        const int64_t head = s.head(p);
         const int n = s.rows(p) * CPR;
 #pragma unroll
         for (int i = 0; i < QC; ++i) {
             const int x = tid + i * NT;
-            qn[i] = x < n ? reinterpret_cast<const uint4*>(q)[x] : make_uint4(0, 0, 0, 0);
+            qn[i] = x < n ? q[query_piece<M>(p, head, x / CPR, x % CPR)] : make_uint4(0, 0, 0, 0);
         }
     };
     auto put_q = [&]() {
@@ -930,7 +959,7 @@ __global__ void __launch_bounds__(NT, M::BLOCKS) paged_attn_kernel(const Params 
         const int rows = seg.rows(p);
         const int64_t head0 = seg.head(p);
         const bool whole = seg.t0 == 0 && seg.t1 == seg.nu;
-        Part<M::ROWS, D>* part = static_cast<Part<M::ROWS, D>*>(p.parts) + 2 * c + (seg.t0 == 0);
+        PartOf<M>* part = static_cast<PartOf<M>*>(p.parts) + 2 * c + (seg.t0 == 0);
         if (!whole && seg.t0 == 0 && tid == 0)
             p.headers[c] = {(int32_t)head0, (int16_t)rows,
                             (int16_t)(longs.worker_of(seg.u + seg.nu - 1) - c + 1)};
@@ -953,29 +982,30 @@ __global__ void __launch_bounds__(NT, M::BLOCKS) paged_attn_kernel(const Params 
             const int row0 = pass * PR, n = min(rows - row0, np * PR);
             for (int i = tid; i < n * (D / 4); i += NT) {
                 const int r = i / (D / 4), e = i % (D / 4) * 4, row = row0 + r;
+                const int mr = max_row<M>(row, e);
                 float mx = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w][row]);
+                for (int w = 0; w < NW; ++w) mx = fmaxf(mx, wm[w][mr]);
                 const float base = mx == -INFINITY ? 0.f : mx;
                 float a[4] = {}, z = 0.f;
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    const float f = ex2(wm[w][row] - base);
+                    const float f = ex2(wm[w][mr] - base);
                     const float4 x = *reinterpret_cast<const float4*>(wput[w] + put_place(D, r, e));
                     a[0] += x.x * f;
                     a[1] += x.y * f;
                     a[2] += x.z * f;
                     a[3] += x.w * f;
-                    z += wl[w][row] * f;
+                    z += wl[w][mr] * f;
                 }
                 if (whole) {
-                    put_out<T>(p, head0 + row, D, e, a, mx, z);
+                    put_out<M>(p, head0, row, e, a, mx, z);
                 } else {
                     *reinterpret_cast<float4*>(&part->a[row][e]) =
                         make_float4(a[0], a[1], a[2], a[3]);
-                    if (e == 0) {
-                        part->m[row] = mx;
-                        part->l[row] = z;
+                    if (e % M::DH == 0) {
+                        part->m[mr] = mx;
+                        part->l[mr] = z;
                     }
                 }
             }
@@ -985,18 +1015,20 @@ __global__ void __launch_bounds__(NT, M::BLOCKS) paged_attn_kernel(const Params 
     }
 }
 
-// Row r of the n parts, to query row `head`: a warp a quarter of the parts, a lane D / 32
-// dimensions. All that a row is made of is on its way before any of it is looked at, up to 32 parts.
+// Row r of the n parts, to row r of the outputs from `head` on: a warp a quarter of the parts, a lane
+// D / 32 dimensions.  All that a row is made of is on its way before any of it is looked at, up to 32
+// parts.
 template <class M>
-__device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M::D>* parts, int n,
-                                         int r, int64_t head) {
+__device__ __forceinline__ void join_row(const Params& p, const PartOf<M>* parts, int n, int r,
+                                         int64_t head) {
     using T = typename M::T;
-    constexpr int D = M::D, E = D / 32, UN = 8, GRID = 148 * M::BLOCKS, PER = (GRID + NT - 1) / NT;
-    __shared__ float w[GRID];                              // the parts' weights
-    __shared__ float sums[NW][D], red[2][NW];
+    constexpr int D = M::D, E = D / 32, EH = E / M::HEADS, UN = 8, GRID = 148 * M::BLOCKS;
+    constexpr int PER = (GRID + NT - 1) / NT, H = M::HEADS;
+    __shared__ float w[H][GRID];                           // the parts' weights
+    __shared__ float sums[NW][D], red[2][H][NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // part k: the tail of block c, then the heads of those that follow
-    float x[UN][E], m[PER], l[PER];
+    float x[UN][E], m[H][PER], l[H][PER];
     auto fetch = [&](int k0) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
@@ -1007,30 +1039,39 @@ __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M:
         }
     };
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int k = tid + i * NT;
-        m[i] = k < n ? parts[2 * k + (k == 0)].m[r] : -INFINITY;
-        l[i] = k < n ? parts[2 * k + (k == 0)].l[r] : 0.f;
-    }
-    fetch(warp);
-    float mx = m[0];
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-    for (int i = 1; i < PER; ++i) mx = fmaxf(mx, m[i]);
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    if (lane == 0) red[0][warp] = mx;
+        for (int i = 0; i < PER; ++i) {
+            const int k = tid + i * NT;
+            m[h][i] = k < n ? parts[2 * k + (k == 0)].m[h * M::ROWS + r] : -INFINITY;
+            l[h][i] = k < n ? parts[2 * k + (k == 0)].l[h * M::ROWS + r] : 0.f;
+        }
+    fetch(warp);
+    float mx[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        mx[h] = m[h][0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) mx[h] = fmaxf(mx[h], m[h][i]);
+        for (int o = 16; o; o >>= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(~0u, mx[h], o));
+        if (lane == 0) red[0][h][warp] = mx[h];
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NW; ++i) mx = fmaxf(mx, red[0][i]);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float z = 0.f;
+    for (int h = 0; h < H; ++h) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const float f = ex2(m[i] - base);
-        if (tid + i * NT < n) w[tid + i * NT] = f;
-        z += f * l[i];
+        for (int i = 0; i < NW; ++i) mx[h] = fmaxf(mx[h], red[0][h][i]);
+        const float base = mx[h] == -INFINITY ? 0.f : mx[h];
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const float f = ex2(m[h][i] - base);
+            if (tid + i * NT < n) w[h][tid + i * NT] = f;
+            z += f * l[h][i];
+        }
+        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
+        if (lane == 0) red[1][h][warp] = z;
     }
-    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(~0u, z, o);
-    if (lane == 0) red[1][warp] = z;
     __syncthreads();
     float a[E] = {};
     for (int k0 = warp; k0 < n; k0 += NW * UN) {
@@ -1038,24 +1079,29 @@ __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M:
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
             const int k = k0 + i * NW;
-            const float f = k < n ? w[k] : 0.f;
+            float f[H];
 #pragma unroll
-            for (int e = 0; e < E; ++e) a[e] = fmaf(f, x[i][e], a[e]);
+            for (int h = 0; h < H; ++h) f[h] = k < n ? w[h][k] : 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[e] = fmaf(f[e / EH], x[i][e], a[e]);
         }
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) sums[warp][lane + 32 * e] = a[e];
     __syncthreads();
-    z = 0.f;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) z += red[1][i];
     if (tid < D) {
-        float y = 0.f;
+        const int h = tid / M::DH;
+        float y = 0.f, z = 0.f, top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NW; ++i) y += sums[i][tid];
-        static_cast<T*>(p.o)[head * D + tid] = from_f32<T>(y / z);
+        for (int i = 0; i < NW; ++i) {
+            y += sums[i][tid];
+            z += red[1][h][i];
+            top = fmaxf(top, red[0][h][i]);
+        }
+        const int64_t row = head + (H == 1 ? 0 : h * p.G) + r;
+        static_cast<T*>(p.o)[row * M::DH + tid % M::DH] = from_f32<T>(y / z);
+        if (p.lse && tid % M::DH == 0) p.lse[row] = (top + log2f(z)) * LN2;
     }
-    if (p.lse && tid == 0) p.lse[head] = (mx + log2f(z)) * LN2;
 }
 
 // Blocks (c, y) join the parts of the pair that block c of the kernel above began and did not
@@ -1063,14 +1109,14 @@ __device__ __forceinline__ void join_row(const Params& p, const Part<M::ROWS, M:
 template <class M>
 __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
     using T = typename M::T;
-    constexpr int D = M::D;
+    constexpr int DH = M::DH;
     const int tid = threadIdx.x, c = blockIdx.x;
     // sequences without keys: zeros, with nothing to wait for
     for (int b = c; b < p.table.S; b += 148 * M::BLOCKS)
         if (units_of(p, b) == 0)
             for (int i = blockIdx.y; i < p.Hq; i += gridDim.y) {
-                for (int e = tid; e < D; e += NT)
-                    static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * D + e] = from_f32<T>(0.f);
+                for (int e = tid; e < DH; e += NT)
+                    static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * DH + e] = from_f32<T>(0.f);
                 if (p.lse && tid == 0) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
             }
     // every block waits: the end of this kernel is to mean the end of both
@@ -1078,8 +1124,7 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
     const Header h = p.headers[c];
     for (int r = blockIdx.y; r < h.rows; r += gridDim.y) {
         __syncthreads();
-        join_row<M>(p, static_cast<const Part<M::ROWS, D>*>(p.parts) + 2 * c, h.parts, r,
-                    (int64_t)h.head + r);
+        join_row<M>(p, static_cast<const PartOf<M>*>(p.parts) + 2 * c, h.parts, r, h.head);
     }
 }
 
@@ -1113,6 +1158,14 @@ int rows_of(bool bf16, int G) {
     return (rows + step - 1) / step * step;
 }
 
+// Whether two heads of 64 dimensions can be worked on as one row of 128, where a group's query rows
+// are one tile: they lie next to one another (see Bf16Math).  A key of one such head is a piece of 128
+// bytes, which HBM serves at 0.84 of the rate of a plain copy: 32 sequences of 50000 tokens, 8 such
+// heads, 573 us one by one and 487 two by two.
+bool two_heads(bool bf16, int d, int G, const PagedPool& pool) {
+    return bf16 && d == 64 && G <= 8 && pool.H % 2 == 0 && pool.sh == 128;
+}
+
 template <int D>
 cudaError_t launch_d(bool bf16, int rows, Params& p, cudaStream_t stream) {
     if (bf16) switch (rows) {
@@ -1132,7 +1185,8 @@ cudaError_t launch_d(bool bf16, int rows, Params& p, cudaStream_t stream) {
 
 size_t paged_attn_workspace(bool bf16, int Hq, int Hkv, int d) {
     const size_t head = (MAX_GRID * sizeof(Header) + 255) / 256 * 256;
-    return head + (size_t)2 * MAX_GRID * rows_of(bf16, Hq / Hkv) * (d + 2) * sizeof(float);
+    const int G = Hq / Hkv, heads = bf16 && d == 64 && G <= 8 ? 2 : 1;   // whatever the strides
+    return head + (size_t)2 * MAX_GRID * rows_of(bf16, G) * heads * (d + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
@@ -1150,6 +1204,11 @@ cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream) {
     p.status = a.status;
     p.headers = static_cast<Header*>(a.workspace);
     p.parts = static_cast<unsigned char*>(a.workspace) + (MAX_GRID * sizeof(Header) + 255) / 256 * 256;
+    if (two_heads(a.bf16, a.d, p.G, a.pool)) {
+        p.pool.H /= 2;
+        p.pool.sh *= 2;
+        return launch<Bf16Math<128, 1, 2>>(p, stream);
+    }
     const int rows = rows_of(a.bf16, p.G);
     return a.d == 64 ? launch_d<64>(a.bf16, rows, p, stream)
                      : launch_d<128>(a.bf16, rows, p, stream);

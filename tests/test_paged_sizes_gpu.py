@@ -412,3 +412,35 @@ def test_captured_upkeep(P):
         n = c.compact()
         assert np.array_equal(pos.cpu().numpy(), rpos) and int(n_live) == n
         dev.same_as(c)
+
+
+def test_attention_neighbouring_heads_of_64():
+    """Heads of 64 dimensions that lie next to one another: what is not finite in one does not reach
+    the other, whichever it is; and pools where they lie apart, or further apart than they are wide."""
+    G = lib()
+    for H, G_ in ((2, 3), (4, 8), (6, 1)):
+        c = filled([100, 3, 2000], 16, H, 64, BF16, seed=95)
+        c.v[c.table[0, 2], 5, 0, 7] = float("inf")
+        c.v[c.table[2, 9], 1, 1, 63] = float("nan")
+        q = queries(3, H * G_, 64, BF16, 95)
+        k1 = c.k.clone()
+        k1[c.table[0, 1], 3, 1] = float("inf")            # head 1: scores of +-inf or NaN
+        dev = Dev(c)
+        o, lse = G.gret_paged_attention_decode(q, dev.lens, dev.table, k1.cuda(), dev.v, lse=True)
+        assert (o[0, :G_, 7] == float("inf")).all() and torch.isnan(o[2, G_:2 * G_, 63]).all()
+        odd = torch.zeros_like(o, dtype=torch.bool)
+        odd[0, :G_, 7] = odd[2, G_:2 * G_, 63] = odd[0, G_:2 * G_] = True
+        assert torch.isfinite(o[~odd]).all()
+        assert torch.isfinite(lse[1:]).all() and torch.isfinite(lse[0, :G_]).all()
+    c = filled([700, 0, 33, 64], 16, 4, 64, BF16, seed=96)
+    dev, q = Dev(c), queries(4, 20, 64, BF16, 96)
+    o, lse = dev.decode(q)
+    check(c, q, o, lse)
+    for wide in ((16, 4, 128), (16, 4, 64), (20, 6, 72)):
+        kw, vw = (torch.full((len(c.ref),) + wide, float("nan"), dtype=BF16, device="cuda")
+                  for _ in range(2))
+        kw, vw = kw[:, :16, :4, :64], vw[:, :16, :4, :64]
+        kw.copy_(dev.k)
+        vw.copy_(dev.v)
+        o, lse = G.gret_paged_attention_decode(q, dev.lens, dev.table, kw, vw, lse=True)
+        check(c, q, o, lse)
