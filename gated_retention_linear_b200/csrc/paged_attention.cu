@@ -51,8 +51,11 @@ namespace {
 constexpr int NT = 128;
 constexpr int NW = NT / 32;
 constexpr int UNIT = 32;               // keys of one unit of work
-constexpr int SHORT_TILES = 8;         // pairs of up to so many are worked on by single warps,
-constexpr int MIN_SHORT = 592;         // where there are at least so many of them
+// Pairs of up to so many tiles are worked on by single warps, where there are at least so many of
+// them: half of the GPU's 1184 warps.  By warps and by blocks, in us: 640 pairs of 5 to 20 keys 8.3
+// and 10.8, of 100 to 128 14.4 and 16.6; but 320 pairs of 100 to 128 keys 13.8 and 10.6.
+constexpr int SHORT_TILES = 8;
+constexpr int MIN_SHORT = 592;
 constexpr int HALF = 4096;             // bytes of a tile's keys, and of its values
 constexpr int STAGE = 2 * HALF;
 constexpr int MAXROWS_BF16 = 24;       // query rows a block works on at a time: what registers hold
