@@ -19,12 +19,12 @@
 // with no more than 100 tokens: two launches, and the chain length -> page -> keys -> parts -> join.
 //
 // bf16: keys are the M side of the product and the query heads of the group the N side (8 to 24,
-// padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows; p is split
-// into two bf16 parts (hi + lo = p up to 2^-16) because one part alone would put its rounding of
-// 2^-9 on every weight, and O^T = V^T P^T.  Both read their 16-bit tiles from shared memory by
+// padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows; and O^T = V^T
+// P^T with p cut into three bf16 parts of 8 bits, which together are p: the weights enter the
+// product as they are summed up, in fp32.  Both read their 16-bit tiles from shared memory by
 // ldmatrix, the accumulators stay in registers.  From 16 heads a group on the products and the
-// softmax no longer hide behind the loads: 24 heads on one kv head run at 0.58 of the copy
-// bandwidth, 12 of 128 at 0.88.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
+// softmax no longer hide behind the loads: 24 heads on one kv head run at 0.54 of the copy
+// bandwidth, 12 of 128 at 0.81.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
 // the scores and a lane four dimensions for the values; 0.94 of the copy bandwidth at G = 3, 0.85 at
 // 8; at 16 (0.46) the queries' reads from shared memory bound it.
 //
@@ -136,10 +136,9 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+// x cut off after its first 8 bits: a bf16 value.
+__device__ __forceinline__ float top16(float x) {
+    return __uint_as_float(__float_as_uint(x) & 0xffff0000u);
 }
 
 // The arithmetic on a tile of KT keys and values, by one warp.  The tile's row r begins at r * ROWB
@@ -234,7 +233,7 @@ struct Bf16Math {
             }
             // s[i]: key lane/4 (0, 1) and lane/4 + 8 (2, 3), queries 2 (lane & 3) and the next
             const bool ok0 = ok >> (j + lane / 4) & 1, ok1 = ok >> (j + 8 + lane / 4) & 1;
-            uint32_t hi[NI][2], lo[NI][2];
+            uint32_t w[3][NI][2];
             bool up = false;
 #pragma unroll
             for (int i = 0; i < NI; ++i)
@@ -267,23 +266,26 @@ struct Bf16Math {
             }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                float p[4], x[4];
+                float part[3][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float base = m[i][e & 1] == -INFINITY ? 0.f : m[i][e & 1];
-                    p[e] = ex2(s[i][e] - base);
-                    l[i][e & 1] += p[e];
-                    // hi: p cut off after 8 bits.  lo: the rest, and 2^-20 p more, so that it is
-                    // not 0 where p is a bf16 value (0 times an infinite value would be NaN)
-                    const float h = __uint_as_float(__float_as_uint(p[e]) & 0xffff0000u);
-                    x[e] = fmaf(p[e], 0x1p-20f, p[e] - h);
+                    const float p = ex2(s[i][e] - base);
+                    l[i][e & 1] += p;
+                    part[0][e] = top16(p);
+                    const float rest = p - part[0][e];
+                    // no part of a weight above 0 is 0: 0 times an infinite value would be NaN
+                    const float least = fmaf(p, 0x1p-30f, fminf(p, 0x1p-133f));
+                    part[1][e] = fmaxf(top16(rest), least);
+                    part[2][e] = fmaxf(rest - top16(rest), least);
                 }
-                hi[i][0] = transpose8x8(__byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]),
-                                                    0x7632));
-                hi[i][1] = transpose8x8(__byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]),
-                                                    0x7632));
-                lo[i][0] = transpose8x8(pack_bf16(x[0], x[1]));
-                lo[i][1] = transpose8x8(pack_bf16(x[2], x[3]));
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        w[t][i][e] = transpose8x8(
+                            __byte_perm(__float_as_uint(part[t][2 * e]),
+                                        __float_as_uint(part[t][2 * e + 1]), 0x7632));
             }
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -293,8 +295,8 @@ struct Bf16Math {
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
                     const int h = k / KH * NQ + i;
-                    mma_16x8x16(acc[i][k], a, hi[h][0], hi[h][1]);
-                    mma_16x8x16(acc[i][k], a, lo[h][0], lo[h][1]);
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) mma_16x8x16(acc[i][k], a, w[t][h][0], w[t][h][1]);
                 }
             }
         }
