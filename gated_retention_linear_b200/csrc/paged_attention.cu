@@ -21,10 +21,13 @@
 // bf16: keys are the M side of the product and the query heads of the group the N side (8 to 24,
 // padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows; and O^T = V^T
 // P^T with p cut into three bf16 parts of 8 bits, which together are p: the weights enter the
-// product as they are summed up, in fp32.  Both read their 16-bit tiles from shared memory by
-// ldmatrix, the accumulators stay in registers.  From 16 heads a group on the products and the
-// softmax no longer hide behind the loads: 24 heads on one kv head run at 0.54 of the copy
-// bandwidth, 12 of 128 at 0.81.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
+// product as they are summed up, in fp32.  Each 16 keys' products are summed up from 0 and added to
+// the rest by the warp: a tensor core cuts its sums off, so that a long one in its accumulators falls
+// short by a third of 2^-23 a step (65536 keys, 16384 a warp, in two parts: all outputs too small by
+// 1.1e-4).  The third part costs 1 to 8 %, these sums 0 to 15 (the more rows the more).  Both read their 16-bit tiles from shared memory by
+// ldmatrix, the accumulators stay in registers.  From 9 heads a group on the products and the
+// softmax no longer hide behind the loads: 24 heads on one kv head run at 0.47 of the copy
+// bandwidth, 12 of 128 at 0.71.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
 // the scores and a lane four dimensions for the values; 0.94 of the copy bandwidth at G = 3, 0.85 at
 // 8; at 16 (0.46) the queries' reads from shared memory bound it.
 //
@@ -295,8 +298,16 @@ struct Bf16Math {
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
                     const int h = k / KH * NQ + i;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};     // of these 16 keys, the least parts first
 #pragma unroll
-                    for (int t = 0; t < 3; ++t) mma_16x8x16(acc[i][k], a, w[t][h][0], w[t][h][1]);
+                    for (int t = 2; t >= 0; --t) mma_16x8x16(sum, a, w[t][h][0], w[t][h][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float2 x = sm100::add2(make_float2(acc[i][k][e], acc[i][k][e + 1]),
+                                                     make_float2(sum[e], sum[e + 1]));
+                        acc[i][k][e] = x.x;
+                        acc[i][k][e + 1] = x.y;
+                    }
                 }
             }
         }

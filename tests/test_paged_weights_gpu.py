@@ -8,7 +8,7 @@ import torch
 
 from paged_model import Cache
 from parity import bf16_half_ulp
-from test_paged_gpu import BF16, F32, Dev, queries
+from test_paged_gpu import BF16, F32, Dev, lib, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,32 @@ def test_infinite_value_of_a_light_key(d, H, G):
     assert (o[..., 3] == float("inf")).all() and (o[..., 5] == -float("inf")).all()
     o[..., 3] = o[..., 5] = 1
     assert (o == 1).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("H,G,d", [(1, 8, 128), (2, 8, 64), (1, 16, 64), (1, 24, 128)])
+def test_long_sums_are_not_cut_off(H, G, d):
+    """300 rows read the same 65536 keys, some 16000 a warp, whose values are all positive.  Sums that
+    are rounded to 32 bits are off to either side, ones that are cut off all to one: 2048 steps that
+    lose a third of 2^-23 of what is summed up by then, half of the whole on average, make 4e-5.
+
+    The outputs, 1 to 2, are rounded to multiples of 2^-7 and spread over several of them (scores
+    that vary by 2.5 leave some hundred keys that count), so the mean of N errors has a deviation of
+    2^-7 / sqrt(12 N); 6 of them are allowed, and 2^-21 for the arithmetic."""
+    B, n, page = 300, 65536, 64
+    gen = torch.Generator("cuda").manual_seed(G + d)
+    k, v = (torch.randn((n // page, page, H, d), generator=gen, device="cuda") for _ in range(2))
+    v = 1.5 + 0.29 * v.clamp(-1.7, 1.7)
+    k, v = k.to(BF16), v.to(BF16)
+    q = torch.randn((B, H * G, d), generator=gen, device="cuda") * 2.5
+    q = q.to(BF16)
+    table = torch.randperm(n // page, generator=gen, device="cuda").int().expand(B, -1).contiguous()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    o, _ = lib().gret_paged_attention_decode(q, lens, table, k, v)
+    off = 0.0
+    for h in range(H):
+        kk, vv = k[:, :, h].reshape(n, d).double(), v[:, :, h].reshape(n, d).double()
+        for qh, oh in zip(q[:, h * G:(h + 1) * G].split(30), o[:, h * G:(h + 1) * G].split(30)):
+            want = torch.softmax(qh.double() @ kk.T * d ** -0.5, -1) @ vv
+            assert want.std() > 2.0 ** -7
+            off += float((oh.double() - want).sum())
+    assert abs(off / o.numel()) <= 6 * 2.0 ** -7 / math.sqrt(12 * o.numel()) + 2.0 ** -21
