@@ -485,7 +485,8 @@ def gret_paged_resize(delta, seq_lens, page_table, ref, k_pages, v_pages, head_m
     last page that it shares; shrinking drops pages.  delta, seq_lens int32 [S], page_table int32 [S,
     max_pages], ref int32 [P]; all but delta, and the pool, are updated in place.  Returns pos
     int32 [S]: a grown row's old length, where its new tokens go, and -1 for the others (among them
-    rows refused because the pool or the table is full, which stay as they are)."""
+    rows refused because the pool or the table is full, or because the last page that they would
+    write on in is none or counts as free; they stay as they are)."""
     return _paged.resize(delta, seq_lens, page_table, ref, k_pages, v_pages, head_major, pos, status,
                          workspace, stream)
 

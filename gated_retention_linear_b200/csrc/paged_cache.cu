@@ -404,26 +404,30 @@ __device__ __forceinline__ int64_t needs_of(const PagedResizeArgs& a, int s0, in
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            fits[u] = !c[u].bad && c[u].n1 > c[u].n0 &&
-                      c[u].n1 <= (int64_t)a.table.max_pages << shift;
+            const bool grows = !c[u].bad && c[u].n1 > c[u].n0;
+            fits[u] = grows && c[u].n1 <= (int64_t)a.table.max_pages << shift;
+            if (lead && c[u].bad) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
+            if (lead && grows && !fits[u]) paged_flag(a.status, GRET_PAGED_TABLE_FULL);
             id[u] = -1;
             if (fits[u] && (c[u].n0 & ((1 << shift) - 1))) {
                 id[u] = a.table.entries[(sb + u) * a.table.stride + (c[u].n0 >> shift)];
                 if ((unsigned)id[u] >= (unsigned)a.pool.n_pages) {
                     if (lead) paged_flag(a.status, GRET_PAGED_BAD_PAGE);
                     id[u] = -1;
+                    fits[u] = false;
                 }
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) count[u] = id[u] >= 0 ? a.ref[id[u]] : 0;
+        for (int u = 0; u < U; ++u) count[u] = id[u] >= 0 ? a.ref[id[u]] : 1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = sb + u;
             if (s >= s1) break;
-            if (lead && c[u].bad) paged_flag(a.status, GRET_PAGED_BAD_LENGTH);
-            if (lead && !c[u].bad && c[u].n1 > c[u].n0 && !fits[u])
-                paged_flag(a.status, GRET_PAGED_TABLE_FULL);
+            if (count[u] <= 0) {                 // free, they say: this call may hand it out
+                if (lead) paged_flag(a.status, GRET_PAGED_BAD_COUNT);
+                fits[u] = false;
+            }
             const int c0 = pages_of(c[u].n0, shift), c1 = pages_of(c[u].n1, shift);
             const bool copies = count[u] > 1;
             const int need = fits[u] ? c1 - c0 + copies : 0;

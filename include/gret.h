@@ -406,8 +406,9 @@ gret_status_t gret_paged_append(
  * in use (copy on write).  A row that shrinks drops the pages past its new length (ref - 1, entry
  * -1), and one shrunk to 0 has given everything back.  Pages dropped by a call can be taken from
  * the next call on.  Not grown, and left as they are with pos = -1: a row past max_pages
- * (TABLE_FULL), and a row that needs pages when those asked for by the rows up to it exceed the
- * pages that are free (NO_PAGES).  pos = -1 for every row that does not grow.
+ * (TABLE_FULL), a row whose partly filled last page is no page or has ref 0 (BAD_PAGE, BAD_COUNT),
+ * and a row that needs pages when those asked for by the rows up to it exceed the pages that are
+ * free (NO_PAGES).  pos = -1 for every row that does not grow.
  */
 size_t gret_paged_resize_workspace_size(int S);
 gret_status_t gret_paged_resize(
