@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(NT) fork_kernel(const PagedForkArgs a) {
         int32_t* to = a.table.entries + d * a.table.stride;
         constexpr int U = 4;
         for (int j0 = blockIdx.y * NT * U; j0 < held; j0 += gridDim.y * NT * U) {
-            int id[U];
+            int id[U], had[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int j = j0 + u * NT + tid;
@@ -712,12 +712,16 @@ __global__ void __launch_bounds__(NT) fork_kernel(const PagedForkArgs a) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int j = j0 + u * NT + tid;
+                had[u] = 1;
                 if (j >= held) continue;
                 to[j] = id[u];
                 if (j < lo || j >= hi) continue;
-                if ((unsigned)id[u] < (unsigned)a.n_pages) atomicAdd(&a.ref[id[u]], add);
+                if ((unsigned)id[u] < (unsigned)a.n_pages) had[u] = atomicAdd(&a.ref[id[u]], add);
                 else paged_flag(a.status, GRET_PAGED_BAD_PAGE);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (had[u] <= 0) paged_flag(a.status, GRET_PAGED_BAD_COUNT);
         }
         if (!SHARE) {
             __syncthreads();                      // every thread has read the lengths

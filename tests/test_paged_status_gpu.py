@@ -40,3 +40,24 @@ def test_resize_bad_last_page(S):
     assert np.array_equal(dev.table.cpu().numpy(), want_table)
     assert np.array_equal(dev.ref.cpu().numpy(), before)
     assert (pos[5:] == i32(lens[5:])).all()
+
+
+@pytest.mark.parametrize("pages,children", [(6, 3), (9000, 3), (3000, 1500)])
+def test_fork_counts_page_that_counts_as_free(pages, children):
+    """Forks that add one by one, few long rows, and many rows of one source."""
+    G = lib()
+    lens = [pages, pages] + [0] * children
+    for bad in (True, False):
+        c = filled(lens, 1, 1, 8, F32, seed=32, spare=1)
+        dev = Dev(c)
+        if bad:
+            c.ref[c.table[0, pages // 2]] = 0
+            dev.ref.copy_(i32(c.ref))
+        dst = np.arange(2, 2 + children)
+        src = np.zeros(children, np.int32)
+        G.gret_paged_fork(i32(src), i32(dst), dev.lens, dev.table, dev.ref, 1, status=dev.status)
+        c.table[dst] = c.table[0]
+        c.lens[dst] = pages
+        c.ref[c.table[0, :pages]] += children
+        dev.same_as(c)
+        assert G.gret_paged_status(dev.status) == (G.GRET_PAGED_BAD_COUNT if bad else 0)
