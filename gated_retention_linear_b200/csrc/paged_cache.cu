@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(NT) fork_lengths_kernel(const PagedForkArgs a)
 // by HBM but for small pools: 16400 pages of 64 KB moved in 338 us (6.3 TB/s), 240 in 11.
 
 // The plan in the workspace: {L, pages to move}, then by page: the k-th hole, the page in use of
-// rank r, the rank of a page in use past L (-1: free).
+// rank r (of those past L), the rank of a page in use (-1: free).
 struct CompactPlan {
     int32_t *counts, *holes, *used, *rank;
 };
@@ -786,12 +786,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(PNT, 1)
                 const int at = ch.entry(q0 + lane) + u;
                 if (at < 0 || at >= P) continue;
                 if (at == L) plan.counts[1] = h[u];    // holes below L = pages in use past it
-                if (at < L) {
-                    if (x[u] == 0) plan.holes[h[u]] = at;
-                } else {
-                    plan.rank[at] = x[u] == 0 ? -1 : at - h[u];
-                    if (x[u] != 0) plan.used[at - h[u]] = at;
-                }
+                plan.rank[at] = x[u] == 0 ? -1 : at - h[u];
+                if (at < L && x[u] == 0) plan.holes[h[u]] = at;
+                if (at >= L && x[u] != 0) plan.used[at - h[u]] = at;
             }
         }
     }
@@ -836,11 +833,11 @@ __global__ void __launch_bounds__(NT) compact_move_kernel(const PagedCompactArgs
             const int id = row[j];
             if ((unsigned)id >= (unsigned)a.pool.n_pages) {
                 paged_flag(a.status, GRET_PAGED_BAD_PAGE);
-            } else if (id >= L) {
-                const int r = plan.rank[id];
-                if (r < 0) paged_flag(a.status, GRET_PAGED_BAD_COUNT);
-                else row[j] = plan.holes[r - (L - moves)];
+                continue;
             }
+            const int r = plan.rank[id];       // as of before the moves, for pages below L too
+            if (r < 0) paged_flag(a.status, GRET_PAGED_BAD_COUNT);
+            else if (id >= L) row[j] = plan.holes[r - (L - moves)];
         }
     }
 }

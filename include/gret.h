@@ -342,8 +342,8 @@ gret_status_t gret_swa_decode_step(const void* q, const void* k, const void* v, 
  *   ref               int32 [n_pages], the number of sequences that hold a page.  0 means free:
  *                     nothing else says so, and a pool starts with zeros.
  *   status            one int32 on the device, or NULL.  Kernels OR GRET_PAGED_* bits into it and
- *                     never clear it; what a bit reports was left out, nothing out of range is
- *                     read or written.
+ *                     never clear it.  Nothing out of range is read or written; what else a bit
+ *                     says is given with the calls.
  *
  * page_size is a power of two up to 1024, S <= 16384, n_pages <= 2^30 (GRET_ERR_UNSUPPORTED
  * otherwise).  k_pages, v_pages, the strides in bytes and d values in bytes are multiples of 16;
@@ -353,12 +353,15 @@ gret_status_t gret_swa_decode_step(const void* q, const void* k, const void* v, 
  * Results do not depend on timing.
  */
 enum {
-    GRET_PAGED_BAD_PAGE = 1,    /* a page id outside [0, n_pages): its tokens were left out     */
+    GRET_PAGED_BAD_PAGE = 1,    /* a page id outside [0, n_pages): left out                     */
     GRET_PAGED_BAD_LENGTH = 2,  /* a length or position that the table cannot hold              */
     GRET_PAGED_NO_PAGES = 4,    /* the pool ran out: the row was not grown                      */
     GRET_PAGED_TABLE_FULL = 8,  /* a row would pass max_pages: it was not grown                 */
     GRET_PAGED_BAD_ROW = 16,    /* a pair of gret_paged_fork was refused                        */
-    GRET_PAGED_BAD_COUNT = 32   /* a page that is held has ref 0                                */
+    GRET_PAGED_BAD_COUNT = 32   /* a page that is held has ref 0.  Found where a call has to do */
+                                /* with the count: of pages that resize drops (the count stays  */
+                                /* 0) or goes on writing on, that fork shares, that compact     */
+                                /* finds in the table.  Append and attention read no counts     */
 };
 
 /*
@@ -433,7 +436,9 @@ gret_status_t gret_paged_fork(
 /*
  * Move the pages in use to the front of the pool.  With L pages in use (n_live[0] = L afterwards),
  * the k-th page in use past index L moves to the k-th free page below L; ref and the table's
- * entries follow.  Pages from L on are free afterwards, so that their memory can be given up.
+ * entries follow.  Pages from L on are free afterwards, so that their memory can be given up.  An
+ * entry that names a page with ref 0 stays as it is (BAD_COUNT): the page is free, and another may
+ * have been moved onto it.
  */
 size_t gret_paged_compact_workspace_size(int n_pages);
 gret_status_t gret_paged_compact(

@@ -2,8 +2,9 @@
 or whose count says that nobody holds it."""
 import numpy as np
 import pytest
+import torch
 
-from test_paged_gpu import F32, Dev, filled, i32, lib
+from test_paged_gpu import BF16, F32, Dev, filled, i32, lib
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,39 @@ def test_fork_counts_page_that_counts_as_free(pages, children):
         c.ref[c.table[0, :pages]] += children
         dev.same_as(c)
         assert G.gret_paged_status(dev.status) == (G.GRET_PAGED_BAD_COUNT if bad else 0)
+
+
+@pytest.mark.parametrize("where", ["front", "behind", "both"])
+def test_compact_held_page_that_counts_as_free(where):
+    """Pages that a row holds and whose count is 0, below the pages in use afterwards and past them:
+    reported; the entry stays, all else moves as if nobody held them."""
+    G = lib()
+    c = filled([64, 48, 40, 8], 8, 2, 8, BF16, seed=33, spare=20)
+    L = int((c.ref > 0).sum()) - 1
+    row, j = np.nonzero((c.table >= 0) & ((c.table < L - 1) if where == "front" else (c.table >= L)))
+    held = [(int(row[0]), int(j[0]))]
+    if where == "both":
+        row, j = np.nonzero((c.table >= 0) & (c.table < L - 2))
+        held.append((int(row[0]), int(j[0])))
+    ids = [int(c.table[h]) for h in held]
+    dev = Dev(c)
+    for i in ids:
+        dev.ref[i] = c.ref[i] = 0
+    n = G.gret_paged_compact(dev.lens, dev.table, dev.ref, dev.k, dev.v, status=dev.status)
+    assert G.gret_paged_status(dev.status) == G.GRET_PAGED_BAD_COUNT
+    was = c.table.copy()
+    assert int(n) == c.compact()
+    for h, i in zip(held, ids):
+        c.table[h] = i
+    assert (c.table != was).any()
+    dev.same_as(c)
+
+
+def test_compact_sound_cache_reports_nothing():
+    G = lib()
+    c = filled([64, 0, 40, 8, 1], 8, 2, 8, BF16, seed=34, spare=40)
+    dev = Dev(c)
+    n = G.gret_paged_compact(dev.lens, dev.table, dev.ref, dev.k, dev.v, status=dev.status)
+    assert int(n) == c.compact() and G.gret_paged_status(dev.status) == 0
+    dev.same_as(c)
+    assert torch.equal(torch.sort(dev.ref, descending=True).values, dev.ref)
