@@ -486,7 +486,8 @@ def gret_paged_resize(delta, seq_lens, page_table, ref, k_pages, v_pages, head_m
     max_pages], ref int32 [P]; all but delta, and the pool, are updated in place.  Returns pos
     int32 [S]: a grown row's old length, where its new tokens go, and -1 for the others (among them
     rows refused because the pool or the table is full, or because the last page that they would
-    write on in is none or counts as free; they stay as they are)."""
+    write on in is none or counts as free; they stay as they are); a pos that is given must not be
+    delta or seq_lens."""
     return _paged.resize(delta, seq_lens, page_table, ref, k_pages, v_pages, head_major, pos, status,
                          workspace, stream)
 

@@ -463,6 +463,12 @@ gret_status_t paged_pool(const void* k_pages, const void* v_pages, int64_t sp, i
     return GRET_OK;
 }
 
+// Whether the na int32 at a and the nb at b share memory.
+bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + 4 * nb && y < x + 4 * na;
+}
+
 gret_status_t launched(cudaError_t e) { return e == cudaSuccess ? GRET_OK : GRET_ERR_CUDA; }
 
 }  // namespace
@@ -578,6 +584,9 @@ gret_status_t gret_paged_resize(
         return GRET_ERR_ALIGNMENT;
     if (!workspace || workspace_bytes < gret_paged_resize_workspace_size(S))
         return GRET_ERR_WORKSPACE;
+    // written by some blocks while others still read these
+    if (overlap(pos, S, delta, S) || overlap(pos, S, seq_lens, S) || overlap(pos, S, ref, n_pages))
+        return GRET_ERR_INVALID_ARG;
     a.delta = delta;
     a.seq_lens = seq_lens;
     a.pos = pos;

@@ -411,7 +411,8 @@ gret_status_t gret_paged_append(
  * the next call on.  Not grown, and left as they are with pos = -1: a row past max_pages
  * (TABLE_FULL), a row whose partly filled last page is no page or has ref 0 (BAD_PAGE, BAD_COUNT),
  * and a row that needs pages when those asked for by the rows up to it exceed the pages that are
- * free (NO_PAGES).  pos = -1 for every row that does not grow.
+ * free (NO_PAGES).  pos = -1 for every row that does not grow.  pos shares no memory with delta,
+ * seq_lens or ref (GRET_ERR_INVALID_ARG).
  */
 size_t gret_paged_resize_workspace_size(int S);
 gret_status_t gret_paged_resize(
