@@ -1,6 +1,7 @@
 """More of what the paged cache's calls refuse on the host, each refusal told by its own message or
 status; on the CPU, where nothing is launched."""
 import pytest
+import torch
 
 from test_paged_cpu import POOL, TABLE, lib
 
@@ -15,3 +16,93 @@ def test_resize_pos_of_its_own(want, pos):
     a = dict(delta=1024, lens=2048, S=4, **TABLE, ref=4096, **POOL, H=8, d=128, pos=pos, status=None,
              ws=8192, wsb=16, stream=None)
     assert G._lib.gret_paged_resize(*a.values()) == want
+
+
+KP = torch.zeros((4, 16, 2, 64))
+Q, LENS = torch.zeros((3, 6, 64)), torch.zeros(3, dtype=torch.int32)
+PT, REF = torch.zeros((3, 5), dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+KV = Q[:, :2]
+
+
+def decode(q=Q, lens=LENS, table=PT, kp=KP, vp=KP, **kw):
+    return lib().gret_paged_attention_decode(q, lens, table, kp, vp, **kw)
+
+
+def append(k=KV, v=KV, pos=LENS, table=PT, kp=KP, vp=KP, **kw):
+    return lib().gret_paged_append(k, v, pos, table, kp, vp, **kw)
+
+
+def resize(delta=LENS, lens=LENS, table=PT, ref=REF, kp=KP, vp=KP, **kw):
+    return lib().gret_paged_resize(delta, lens, table, ref, kp, vp, **kw)
+
+
+def fork(src=LENS, dst=LENS, lens=LENS, table=PT, ref=REF, page=16):
+    return lib().gret_paged_fork(src, dst, lens, table, ref, page)
+
+
+def compact(lens=LENS, table=PT, ref=REF, kp=KP, vp=KP, **kw):
+    return lib().gret_paged_compact(lens, table, ref, kp, vp, **kw)
+
+
+OTHER_STRIDES = KP.transpose(1, 2).contiguous().transpose(1, 2)
+LAST_APART = torch.zeros((4, 16, 2, 128))[..., ::2]
+Q_RULE = r"q must be contiguous \[B, Hq, d\] with the pool's d and dtype"
+TABLE_RULE = r"page_table must be int32 \[3, max_pages\] with contiguous rows"
+KV_RULE = r"k and v must be \[T, Hkv, d\] with the pool's heads and dtype"
+
+
+@pytest.mark.parametrize("error,message,call", [
+    # the checks come before the one that every tensor is on a GPU: what passes them all gets there
+    (ValueError, "must be on a GPU", lambda: decode()),
+    (ValueError, "must be on a GPU", lambda: append()),
+    (ValueError, "must be on a GPU", lambda: resize()),
+    (ValueError, "must be on a GPU", lambda: fork()),
+    (ValueError, "must be on a GPU", lambda: compact()),
+    (ValueError, "must be on a GPU", lambda: decode(table=PT[:, :1])),
+    (ValueError, "must be on a GPU", lambda: decode(table=torch.zeros((3, 9), dtype=torch.int32)[:, 2:7])),
+    (ValueError, Q_RULE, lambda: decode(q=Q.bfloat16())),
+    (ValueError, Q_RULE, lambda: decode(q=Q[..., :32].contiguous())),
+    (ValueError, Q_RULE, lambda: decode(q=Q[0])),
+    (ValueError, Q_RULE, lambda: decode(q=Q.transpose(0, 1))),
+    (ValueError, TABLE_RULE, lambda: decode(table=PT[:2])),
+    (ValueError, TABLE_RULE, lambda: decode(table=PT.long())),
+    (ValueError, TABLE_RULE, lambda: decode(table=PT[0])),
+    (ValueError, TABLE_RULE, lambda: decode(table=torch.zeros((5, 3), dtype=torch.int32).t())),
+    (ValueError, TABLE_RULE, lambda: append(table=PT.long())),
+    (ValueError, TABLE_RULE, lambda: resize(table=PT[:2])),
+    (ValueError, TABLE_RULE, lambda: fork(table=PT.float())),
+    (ValueError, TABLE_RULE, lambda: compact(table=torch.zeros((4, 5), dtype=torch.int32))),
+] + [
+    (error, message, lambda f=f, kp=kp, vp=vp: f(kp=kp, vp=vp))
+    for f in (decode, append, resize, compact)
+    for error, message, kp, vp in [
+        (ValueError, "must be 4-D and alike", KP, KP[:2]),
+        (ValueError, "must be 4-D and alike", KP[0], KP[0]),
+        (ValueError, "must be 4-D and alike", KP, KP.bfloat16()),
+        (ValueError, "must share strides", KP, OTHER_STRIDES),
+        (ValueError, "the last one 1", LAST_APART, LAST_APART),
+        (TypeError, "must be bfloat16 or float32, got Half", KP.half(), KP.half()),
+    ]
+] + [
+    (ValueError, KV_RULE, lambda: append(k=Q, v=Q)),                       # heads
+    (ValueError, KV_RULE, lambda: append(k=KV[..., :32], v=KV[..., :32])),
+    (ValueError, KV_RULE, lambda: append(v=KV[:2])),
+    (ValueError, KV_RULE, lambda: append(k=KV.bfloat16(), v=KV.bfloat16())),
+    (ValueError, KV_RULE, lambda: append(v=KV.bfloat16())),
+    (ValueError, KV_RULE, lambda: append(k=KV[0], v=KV[0])),
+    (ValueError, "last dimension must be contiguous",
+     lambda: append(k=torch.zeros((3, 2, 128))[..., ::2])),
+    (ValueError, "last dimension must be contiguous",
+     lambda: append(v=torch.zeros((3, 2, 128))[..., ::2])),
+    (ValueError, "window is out of range", lambda: decode(window=2 ** 31)),
+    (ValueError, "page_size is out of range", lambda: fork(page=-2 ** 31 - 1)),
+    (TypeError, "q must be a tensor", lambda: decode(q=[1.0])),
+    (TypeError, "status must be a tensor", lambda: decode(status=0)),
+    (TypeError, "lse must be a tensor", lambda: decode(lse=False)),
+    (TypeError, "cu_seqlens must be a tensor", lambda: append(cu_seqlens=[0, 3])),
+    (TypeError, "pos must be a tensor", lambda: resize(pos=3)),
+    (TypeError, "n_live must be a tensor", lambda: compact(n_live=3)),
+])
+def test_binding_tells_what_is_wrong(error, message, call):
+    with pytest.raises(error, match=message):
+        call()
