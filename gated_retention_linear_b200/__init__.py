@@ -4,9 +4,9 @@ A thin Python binding over the C ABI in include/gret.h (libgret.so, built in-tre
 `python gated_retention_linear_b200/build.py`).  The functions here only marshal arguments:
 they read shapes and strides off torch tensors, allocate outputs and workspaces with torch, pass
 raw device pointers and the current CUDA stream, and raise on a non-OK status.  Every step of
-the computation runs in the library's CUDA kernels; there is no fallback.  The paged cache's
-calls do the same in C++ (csrc/paged_binding.cpp, _paged.so).  If libgret.so or _paged.so is
-missing this import fails.
+the computation runs in the library's CUDA kernels; there is no fallback.  If libgret.so is
+missing this import fails.  The paged cache's calls do the same in C++ (csrc/paged_binding.cpp,
+_paged.so); where that cannot be loaded these calls, and no others, raise ImportError.
 """
 import ctypes
 import os
@@ -16,14 +16,29 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgret.so")
 
-for _path in (LIB_PATH, os.path.join(_HERE, "_paged.so")):
-    if not os.path.exists(_path):
-        raise ImportError("%s not found at %s; build it with `python gated_retention_linear_b200/"
-                          "build.py`" % (os.path.basename(_path), _path))
+if not os.path.exists(LIB_PATH):
+    raise ImportError("libgret.so not found at %s; build it with "
+                      "`python gated_retention_linear_b200/build.py`" % LIB_PATH)
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _paged  # noqa: E402  (needs torch and libgret.so loaded)
+
+
+class _NoBinding:
+    """In place of _paged.so when that cannot be loaded: says so at every call."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError("the paged cache's calls need _paged.so (%s); build it with "
+                          "`python gated_retention_linear_b200/build.py`" % self._why)
+
+
+try:
+    from . import _paged  # needs torch and libgret.so loaded
+except ImportError as e:
+    _paged = _NoBinding(e)
 
 GRET_F32, GRET_BF16 = 0, 1
 STATUS = {0: "GRET_OK", 1: "GRET_ERR_INVALID_ARG", 2: "GRET_ERR_UNSUPPORTED",
@@ -117,7 +132,8 @@ def _check(fn, code):
         raise GretError(fn, code)
 
 
-_paged.set_check(_check)
+if not isinstance(_paged, _NoBinding):
+    _paged.set_check(_check)
 
 
 def _ptr(t):

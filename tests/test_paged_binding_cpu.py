@@ -1,5 +1,10 @@
 """More of what the paged cache's calls refuse on the host, each refusal told by its own message or
 status; on the CPU, where nothing is launched."""
+import os
+import shutil
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -106,3 +111,44 @@ KV_RULE = r"k and v must be \[T, Hkv, d\] with the pool's heads and dtype"
 def test_binding_tells_what_is_wrong(error, message, call):
     with pytest.raises(error, match=message):
         call()
+
+
+def copied_package(tmp_path, *names):
+    import gated_retention_linear_b200 as G
+    src = os.path.dirname(G.__file__)
+    dst = tmp_path / os.path.basename(src)
+    dst.mkdir()
+    for name in names:
+        shutil.copy(os.path.join(src, name), dst / name)
+    return dst
+
+
+@pytest.mark.parametrize("what", ["missing", "not loadable"])
+def test_import_without_the_binding(tmp_path, what):
+    """_paged.so serves the paged cache's calls alone: without it, or with one that does not fit the
+    installed torch, the library imports, everything else works, and those calls say what is wrong."""
+    dst = copied_package(tmp_path, "__init__.py", "libgret.so")
+    if what != "missing":
+        (dst / "_paged.so").write_bytes(b"not a library")
+    code = """
+import torch
+import gated_retention_linear_b200 as G
+assert G.__file__.startswith(%r)
+assert G.gret_prefill_workspace_size(torch.bfloat16, 100, 1, 2, 128, 128) >= 0
+assert G.gret_paged_attention_workspace_size(torch.bfloat16, 24, 8, 128) > 0
+x = torch.zeros(3, dtype=torch.int32)
+pool = torch.zeros((4, 16, 2, 64))
+for call in (lambda: G.gret_paged_attention_decode(pool[0, :3], x, x[None], pool, pool),
+             lambda: G.gret_paged_append(pool[0], pool[0], x, x[None], pool, pool),
+             lambda: G.gret_paged_resize(x, x, x[None], x, pool, pool),
+             lambda: G.gret_paged_fork(x, x, x, x[None], x, 16),
+             lambda: G.gret_paged_compact(x, x[None], x, pool, pool)):
+    try:
+        call()
+    except ImportError as e:
+        assert "_paged.so" in str(e) and "build.py" in str(e), e
+    else:
+        raise AssertionError("no ImportError")
+""" % str(tmp_path)
+    subprocess.run([sys.executable, "-c", code], cwd=tmp_path, check=True,
+                   env={**os.environ, "PYTHONPATH": str(tmp_path)})
