@@ -23,7 +23,6 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 
-
 class _NoBinding:
     """In place of _paged.so when that cannot be loaded: says so at every call."""
 

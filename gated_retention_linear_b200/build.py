@@ -12,6 +12,7 @@ time through the runtime, so the library does not link libcuda.
 """
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import subprocess
@@ -54,8 +55,14 @@ def _compile(src, verbose):
 
 def _build_binding(force):
     src = os.path.join(CSRC, "paged_binding.cpp")
-    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "gret.h")]):
-        return
+    # whose C++ interfaces the binding is compiled against: neither is stable from one to the next
+    tag = "torch %s, %s" % (importlib.metadata.version("torch"), sysconfig.get_config_var("SOABI"))
+    tag_file = os.path.join(BUILD, "paged_binding.tag")
+    if not force and not _stale(BINDING, [src, os.path.join(INCLUDE, "gret.h")]) \
+            and os.path.exists(tag_file):
+        with open(tag_file) as f:
+            if f.read() == tag:
+                return
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     inc = [os.path.join(torch, "include"), sysconfig.get_paths()["include"], INCLUDE,
            os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
@@ -66,6 +73,8 @@ def _build_binding(force):
                       "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB),
                       "-Wl,-rpath,$ORIGIN"], check=True)
     os.replace(tmp, BINDING)
+    with open(tag_file, "w") as f:
+        f.write(tag)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -1,5 +1,6 @@
 """More of what the paged cache's calls refuse on the host, each refusal told by its own message or
 status; on the CPU, where nothing is launched."""
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -152,3 +153,45 @@ for call in (lambda: G.gret_paged_attention_decode(pool[0, :3], x, x[None], pool
 """ % str(tmp_path)
     subprocess.run([sys.executable, "-c", code], cwd=tmp_path, check=True,
                    env={**os.environ, "PYTHONPATH": str(tmp_path)})
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(tmp_path, monkeypatch):
+    """_paged.so uses torch's C++ interface and Python's: build() makes it anew when either is not the
+    one it was made for, when it or what it is made of has changed, and not otherwise."""
+    import gated_retention_linear_b200 as G
+    spec = importlib.util.spec_from_file_location(
+        "build_under_test", os.path.join(os.path.dirname(G.__file__), "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    so = tmp_path / "_paged.so"
+    monkeypatch.setattr(b, "BINDING", str(so))
+    monkeypatch.setattr(b, "BUILD", str(tmp_path))
+    runs = []
+
+    def run(cmd, **kw):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "wb").close()
+
+    monkeypatch.setattr(b.subprocess, "run", run)
+
+    def builds(force=False):
+        n = len(runs)
+        b._build_binding(force)
+        assert so.exists()
+        return len(runs) - n
+
+    assert builds() == 1 and builds() == 0
+    with monkeypatch.context() as m:
+        m.setattr(b.importlib.metadata, "version", lambda name: "2.12.0")
+        assert builds() == 1 and builds() == 0
+    assert builds() == 1 and builds() == 0
+    config = b.sysconfig.get_config_var
+    with monkeypatch.context() as m:
+        m.setattr(b.sysconfig, "get_config_var",
+                  lambda name: "cpython-313" if name == "SOABI" else config(name))
+        assert builds() == 1 and builds() == 0
+    assert builds() == 1 and builds() == 0
+    os.utime(so, (0, 0))                               # older than its source
+    assert builds() == 1 and builds() == 0
+    so.unlink()
+    assert builds() == 1 and builds(force=True) == 1 and builds() == 0
