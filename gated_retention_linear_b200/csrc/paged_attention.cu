@@ -1127,7 +1127,13 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
     using T = typename M::T;
     constexpr int DH = M::DH;
     const int tid = threadIdx.x, c = blockIdx.x;
-    // sequences without keys: zeros, with nothing to wait for
+    wait_for_previous();
+    const Header h = p.headers[c];
+    for (int r = blockIdx.y; r < h.rows; r += gridDim.y) {
+        __syncthreads();
+        join_row<M>(p, static_cast<const PartOf<M>*>(p.parts) + 2 * c, h.parts, r, h.head);
+    }
+    // sequences without keys: zeros
     for (int b = c; b < p.table.S; b += 148 * M::BLOCKS)
         if (units_of(p, b) == 0)
             for (int i = blockIdx.y; i < p.Hq; i += gridDim.y) {
@@ -1135,13 +1141,6 @@ __global__ void __launch_bounds__(NT) paged_join_kernel(const Params p) {
                     static_cast<T*>(p.o)[((int64_t)b * p.Hq + i) * DH + e] = from_f32<T>(0.f);
                 if (p.lse && tid == 0) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
             }
-    // every block waits: the end of this kernel is to mean the end of both
-    wait_for_previous();
-    const Header h = p.headers[c];
-    for (int r = blockIdx.y; r < h.rows; r += gridDim.y) {
-        __syncthreads();
-        join_row<M>(p, static_cast<const PartOf<M>*>(p.parts) + 2 * c, h.parts, r, h.head);
-    }
 }
 
 template <class M>
