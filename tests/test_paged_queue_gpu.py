@@ -1,6 +1,10 @@
 """Calls of the paged cache queued behind one another, every one of their outputs looked at: a kernel
 that starts before the one in front has ended, or a workspace that is used again too early, shows
 in the call that it happens to and not in the last one alone."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -133,3 +137,57 @@ def test_refusals_of_gpu_tensors():
     with pytest.raises(G.GretError, match="INVALID_ARG"):
         res(delta=torch.ones_like(dev.lens), pos=dev.lens)
     dev.same_as(c)
+
+
+@pytest.mark.parametrize("dtype,B,H,G_,d", [
+    (BF16, 3, 2, 3, 128), (BF16, 250, 4, 5, 64), (BF16, 4, 1, 40, 128), (F32, 300, 3, 2, 128),
+    (F32, 5, 2, 20, 64),
+])
+def test_attention_in_place(dtype, B, H, G_, d):
+    """Outputs in the queries' place: no block reads a query after another has written there."""
+    rng = np.random.default_rng(B)
+    c = filled(rng.integers(0, 90, B).tolist() + [3000], 16, H, d, dtype, seed=92)
+    dev, q = Dev(c), queries(B + 1, H * G_, d, dtype, 92)
+    want, _ = dev.decode(q)
+    o, _ = dev.decode(q, o=q)
+    assert o is q and torch.equal(o, want)
+
+
+FIRST_CALL = """
+import torch
+import gated_retention_linear_b200 as G
+dev = "cuda"
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)
+P, page, W, S = %d, 4, 40, 20
+kp, vp = (torch.zeros((P, page, 2, 64), dtype=torch.bfloat16, device=dev) for _ in range(2))
+table, lens, ref = torch.full((S, W), -1, dtype=torch.int32, device=dev), i32([0] * S), i32([0] * P)
+delta, src, dst = i32([9, 2] + [0] * (S - 2)), i32([0]), i32([3])
+k, v = (torch.randn((11, 2, 64), device=dev).bfloat16() for _ in range(2))
+q, cu = torch.randn((S, 6, 64), device=dev).bfloat16(), i32([0, 9] + [11] * (S - 1))
+status, n_live = i32([0]), i32([0])
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    pos = G.gret_paged_resize(delta, lens, table, ref, kp, vp, status=status)
+    G.gret_paged_append(k, v, pos, table, kp, vp, cu_seqlens=cu, status=status)
+    G.gret_paged_fork(src, dst, lens, table, ref, page, status=status)
+    G.gret_paged_compact(lens, table, ref, kp, vp, n_live=n_live, status=status)
+    o, lse = G.gret_paged_attention_decode(q, lens, table, kp, vp, lse=True, status=status)
+graph.replay()
+torch.cuda.synchronize()
+assert lens.tolist() == [9, 2, 0, 9] + [0] * (S - 4) and int(n_live) == 4 and int(status) == 0
+assert pos[:3].tolist() == [0, 0, -1] and ref[:5].tolist() == [2, 2, 2, 1, 0]
+for s, a, b in ((0, 0, 9), (1, 9, 11), (3, 0, 9)):
+    w = torch.einsum("hgd,nhd->hgn", q[s].view(2, 3, 64).float(), k[a:b].float()) / 8
+    want = torch.einsum("hgn,nhd->hgd", torch.softmax(w, 2), v[a:b].float()).reshape(6, 64)
+    assert (o[s].float() - want).abs().max() < 0.03
+    assert (lse[s] - torch.logsumexp(w, 2).reshape(6)).abs().max() < 1e-4
+assert (o[2] == 0).all() and (lse[2] == -float("inf")).all()
+"""
+
+
+@pytest.mark.parametrize("P", [100, 140000])
+def test_first_call_of_a_process_in_a_capture(P):
+    """Nothing that a call does once a process or a device is out of place in a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST_CALL % P], cwd=root, check=True, timeout=300)
