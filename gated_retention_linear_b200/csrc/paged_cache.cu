@@ -202,8 +202,9 @@ __device__ __forceinline__ int rank_free(const Chunks& ch, int* count, int64_t (
     return r.all_y;
 }
 
-// Division by a number known on the host, for dividends below 2^31: with s = ceil(log2 d) and
-// m = floor(2^32 (2^s - d) / d) + 1, n / d = (floor(m n / 2^32) + n) >> s.
+// Division by a number known on the host, for dividends below 2^31, by multiplication (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994): with s = ceil(log2 d)
+// and m = floor(2^32 (2^s - d) / d) + 1, n / d = (floor(m n / 2^32) + n) >> s.
 struct FastDiv {
     uint32_t d, m;
     int s;
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(NT) append_kernel(const PagedAppendArgs a, con
 
 // ---------------------------------------------------------------------------------------------
 // resize: a plan by one cluster (who gets which page), then the whole GPU carries it out.  Latency
-// bounds it: of a step of 256 rows on 20000 pages (9.5 us) the plan takes 7 (rows 1.5, counting 1.4,
+// bounds it: of a step of 256 rows on 20000 pages (9.7 us) the plan takes 7 (rows 1.5, counting 1.4,
 // the cluster's barrier and the sums 1.2, handing out 1.5, the launch the rest) and the copies 2.7;
 // of 1000 rows that come and go on 786433 pages (24 us) counting takes 5.5 (it reads 0.8 TB/s, with
 // 8 blocks or 16: they share one GPC's way to the L2), handing out 6, and the rows' lists 4.
@@ -633,11 +634,14 @@ __global__ void __launch_bounds__(NT, APPLY_SM) resize_apply_kernel(const PagedR
 }
 
 // ---------------------------------------------------------------------------------------------
-// fork.  The copy of the table entries is bound by HBM (L2, for the rows that many share): 512 rows
-// of 7000 entries 12 us, 64 of 50 3.2.  The counts are bound by atomics on one address where many
-// pairs share a source and each adds its 1: there, of the m pairs of a source each adds m to an m-th
-// of its pages.  That takes the pairs' knowing of one another, so that the lengths, by which a pair
-// that has no effect is known, can only be set by a second kernel; small calls go without.
+// fork.  Bound by latency: 64 rows of 50 entries take 2.6 us, 512 of 7000 11.5, of which the copy of
+// the 14 MB of entries would take 2.2.  The rest is the chain of every block before its first entry
+// (the pairs, the rows that they name, their lengths; and once more over all pairs for those that
+// share a source), then that of the second kernel.  Counts of pages that many rows share would be
+// bound by atomics on one address if each pair added its 1: there, of the m pairs of a source each
+// adds m to an m-th of its pages.  That takes the pairs' knowing of one another, so that the lengths,
+// by which a pair that has no effect is known, can only be set by a second kernel; small calls go
+// without.
 
 // The first pair that names each row as its destination (INT_MAX: none).
 __device__ __forceinline__ void first_pairs(const PagedForkArgs& a, int* first) {
@@ -716,8 +720,11 @@ __global__ void __launch_bounds__(NT) fork_kernel(const PagedForkArgs a) {
                 if (j >= held) continue;
                 to[j] = id[u];
                 if (j < lo || j >= hi) continue;
-                if ((unsigned)id[u] < (unsigned)a.n_pages) had[u] = atomicAdd(&a.ref[id[u]], add);
-                else paged_flag(a.status, GRET_PAGED_BAD_PAGE);
+                // the old count is asked for where it can be reported: additions that return it take
+                // a third longer (512 rows of 512 entries, 2 of a source, 3.9 -> 5.1 us)
+                if ((unsigned)id[u] >= (unsigned)a.n_pages) paged_flag(a.status, GRET_PAGED_BAD_PAGE);
+                else if (!a.status) atomicAdd(&a.ref[id[u]], add);
+                else had[u] = atomicAdd(&a.ref[id[u]], add);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -875,9 +882,11 @@ cudaError_t launch_paged_fork(const PagedForkArgs& a, cudaStream_t stream) {
     const int x = a.n < 2 * GRID ? a.n : 2 * GRID;
     cudaError_t e;
     // Without sharing out the counts: one launch, a block a pair.  Measured against two launches, in
-    // us: 64 rows of 76 entries 8 and 11, 512 of 512 11 and 13, 2000 of 1000 15 and 23, 1024 of 2048
-    // 13 and 15; but 512 of 8192 16 and 15, and one row of 32768, which only the other cuts up, 16
-    // and 11.
+    // us, for 2, 8 and 125 rows a source: 64 rows of 76 entries 2.6, 2.8, 2.9 and 5.1, 5.4, 5.5; 512 of
+    // 512 3.9, 5.3, 13.5 and 6.6, 7.2, 7.4; 2000 of 1000 17, 17, 33 and 19, 16, 19; 1024 of 2040 15, 16,
+    // 30 and 14, 11, 10; 512 of 8180 30, 30, 48 and 21, 15, 12; and one row of 32768, which only the
+    // other cuts up, 26 and 6.  How many rows share a source the host does not know: the rule is for
+    // few.
     if (a.table.max_pages <= 8192 && (int64_t)a.n * a.table.max_pages <= FORK_ALONE) {
         e = allow_smem<fork_kernel<false>>(smem, most_smem);
         if (e != cudaSuccess) return e;
