@@ -8,34 +8,37 @@
 //     m = max m_i,  l = sum e^(m_i - m) l_i,  o = sum e^(m_i - m) a_i / l.
 //
 // Bound: HBM, 2 n d values a (sequence, kv head) read once, 2 G flops a value.  That little
-// arithmetic leaves the tensor cores idle for most of the time in any form (14 % busy at G = 3), so
-// the form is chosen for the loads: every warp runs its own ring of cp.async tiles (KT keys and
-// values of one head, 8 KB), two of them always in flight behind the one being worked on and across
-// the borders of sequences, with no barrier between warps but where a (sequence, head) ends;
-// page-table entries are read two tiles ahead of that.  16-byte pieces gathered by lanes take any
-// page size and any stride, where a bulk copy would want one tensor map a layout and at least a page
-// of tokens. Measured, 8 kv heads of 128 in bf16, G = 3: 64 sequences of 200 to 32768 tokens 270 us
-// (6.5 TB/s, what a plain copy reaches), 2 of 524288 645 us; one of 4096 8.9 us, of which 6.7 go by
-// with no more than 100 tokens: two launches, and the chain length -> page -> keys -> parts -> join.
+// arithmetic leaves the tensor cores idle for most of the time in any form (18 % busy at G = 3),
+// so the form is chosen for the loads: every warp runs its own ring of cp.async tiles (KT keys and
+// values of one head, 8 KB), all but one of them always in flight behind the one being worked on
+// and across the borders of sequences, with no barrier between warps but where a (sequence, head)
+// ends; page-table entries are read as many tiles ahead of that.  A ring has three tiles, of two
+// blocks an SM (F32Math::MORE: two tiles, three blocks).  16-byte pieces gathered by lanes take
+// any page size and any stride, where a bulk copy would want one tensor map a layout and at least
+// a page of tokens. Measured, 8 kv heads of 128 in bf16, G = 3: 64 sequences of 200 to 32768
+// tokens 266 to 272 us (6.5 TB/s, what a plain copy reaches), 2 of 524288 646 us; one of 4096 8.9
+// us, of which 6.8 go by with no more than 100 tokens: two launches, and the chain length -> page
+// -> keys -> parts -> join.
 //
 // bf16: keys are the M side of the product and the query heads of the group the N side (8 to 24,
-// padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows; and O^T = V^T
-// P^T with p cut into three bf16 parts of 8 bits, which together are p: the weights enter the
-// product as they are summed up, in fp32.  Each 16 keys' products are summed up from 0 and added to
-// the rest by the warp: a tensor core cuts its sums off, so that a long one in its accumulators falls
-// short by a third of 2^-23 a step (65536 keys, 16384 a warp, in two parts: all outputs too small by
-// 1.1e-4).  The third part costs 1 to 8 %, these sums 0 to 15 (the more rows the more).  Both read their 16-bit tiles from shared memory by
-// ldmatrix, the accumulators stay in registers.  From 9 heads a group on the products and the
-// softmax no longer hide behind the loads: 24 heads on one kv head run at 0.47 of the copy
-// bandwidth, 12 of 128 at 0.71.  fp32: products in packed fp32 on the CUDA cores, a lane a key for
-// the scores and a lane four dimensions for the values; 0.94 of the copy bandwidth at G = 3, 0.85 at
-// 8; at 16 (0.46) the queries' reads from shared memory bound it.
+// padded to a multiple of 8), S^T = K Q^T, so 3 heads cost 8 columns and not 16 rows; and O^T =
+// V^T P^T with p cut into three bf16 parts of 8 bits, which together are p: the weights enter the
+// product as they are summed up, in fp32.  Each 16 keys' products are summed up from 0 and added
+// to the rest by the warp: a tensor core cuts its sums off, so that a long one in its accumulators
+// falls short by 2^-23 or so of itself a step (65536 keys, 16384 a warp, 2048 steps: all outputs
+// too small by 1.1e-4).  The third part takes 1 to 8 % of the time, these sums 0 to 15 (the more
+// rows the more).  Keys and values are read from shared memory by ldmatrix, the sums stay in
+// registers.  From 9 heads a group on the products and the softmax no longer hide behind the
+// loads: 12 of 128 on each of two kv heads run at 0.71 of the copy bandwidth, 24 on one at 0.47,
+// 32 (keys read twice) at 0.33. fp32: products in packed fp32 on the CUDA cores, a lane a key for
+// the scores and a lane four dimensions for the values; 0.95 of the copy bandwidth at G = 3, 0.85
+// at 8; at 16 (0.47) the queries' reads from shared memory bound it.
 //
 // The work is cut into units of UNIT keys of one (sequence, kv head, group of query rows), a pair;
 // the units of the whole batch are dealt out evenly over the grid, in order, so that one long
 // sequence spreads over every SM and a ragged batch stays balanced without the host knowing the
-// lengths.  A block whose range ends inside a (sequence, head) writes its part to the workspace;
-// a second kernel joins the parts in block order, so that results do not depend on timing.  Batches
+// lengths.  A block whose range ends inside a (sequence, head) writes its part to the workspace; a
+// second kernel joins the parts in block order, so that results do not depend on timing.  Batches
 // of many short pairs go to single warps instead (ByWarps).
 #include <cuda_bf16.h>
 #include <limits.h>
@@ -55,8 +58,8 @@ constexpr int NT = 128;
 constexpr int NW = NT / 32;
 constexpr int UNIT = 32;               // keys of one unit of work
 // Pairs of up to so many tiles are worked on by single warps, where there are at least so many of
-// them: half of the GPU's 1184 warps.  By warps and by blocks, in us: 640 pairs of 5 to 20 keys 8.3
-// and 10.8, of 100 to 128 14.4 and 16.6; but 320 pairs of 100 to 128 keys 13.8 and 10.6.
+// them: half of the GPU's 1184 warps.  By warps and by blocks, in us: 640 pairs of 5 to 20 keys 8.7
+// and 11.0, of 100 to 128 15.6 and 17.3; but 320 pairs of 100 to 128 keys 14.7 and 11.2.
 constexpr int SHORT_TILES = 8;
 constexpr int MIN_SHORT = 592;
 constexpr int HALF = 4096;             // bytes of a tile's keys, and of its values
@@ -64,7 +67,10 @@ constexpr int STAGE = 2 * HALF;
 constexpr int MAXROWS_BF16 = 24;       // query rows a block works on at a time: what registers hold
 constexpr int MAXROWS_F32 = 16;
 constexpr int MAX_GRID = 148 * 3;
-constexpr int JOIN_Y = 8;              // blocks a pair of the join: 8 x GRID are in place at once
+// Blocks a pair of the join.  With 2, 4, 8 and 16 of them, calls in us: one sequence of 4096 keys
+// (3 rows a pair) 10.4, 8.9 and no more change; 64 ragged ones of 24 heads on one kv head 84, 77, 75
+// and 74.
+constexpr int JOIN_Y = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -476,7 +482,7 @@ struct F32Math {
 
 // The same with short pairs worked on by single warps.  A block takes 1.5 us and more to end a pair,
 // and one warp little longer for a short one altogether, while the block's others do as much: 187 x
-// 16 pairs of 2 keys 32 -> 16 us, 192 x 16 of 70 keys of 64 dimensions 32 -> 22.  A kernel of its
+// 16 pairs of 2 keys 28 -> 14 us, 192 x 16 of 70 keys of 64 dimensions 28 -> 22.  A kernel of its
 // own, for batches that may have enough such pairs: others would be 3 to 6 % slower for the code
 // that they have no use for.  Not where the rows' sums leave no registers to spare (SPARE): there
 // the kernel would be 9 % slower on batches that are long after all.
@@ -731,7 +737,7 @@ __device__ __forceinline__ Share share_of(const Params& p, DealSmem& sm) {
 }
 
 // A warp's walk over the tiles that it is to load.  A tile's page-table entries are read when it
-// enters the queue `ahead`, two tiles before they are needed: one latency for all of a ring's first
+// enters the queue `ahead`, S - 1 tiles before they are needed: one latency for all of a ring's first
 // tiles.
 template <class M>
 struct Loader {
@@ -1176,7 +1182,7 @@ int rows_of(bool bf16, int G) {
 // Whether two heads of 64 dimensions can be worked on as one row of 128, where a group's query rows
 // are one tile: they lie next to one another (see Bf16Math).  A key of one such head is a piece of 128
 // bytes, which HBM serves at 0.84 of the rate of a plain copy: 32 sequences of 50000 tokens, 8 such
-// heads, 573 us one by one and 487 two by two.
+// heads, 587 us one by one and 479 two by two.
 bool two_heads(bool bf16, int d, int G, const PagedPool& pool) {
     return bf16 && d == 64 && G <= 8 && pool.H % 2 == 0 && pool.sh == 128;
 }

@@ -427,7 +427,8 @@ gret_status_t gret_paged_resize(
  * are copied, ref + 1 each, no key or value moves.  dst[i] must be an empty row (length 0).  Refused
  * (BAD_ROW), and without effect: a row out of range, a destination that is not empty or that an
  * earlier pair names, a source that is a destination of any pair.  A page of the source that has
- * ref 0 is counted for the new rows all the same (BAD_COUNT: its count is one too few).
+ * ref 0 is counted for the new rows all the same (BAD_COUNT: its count is one too few); an entry
+ * that is no page is copied as it is (BAD_PAGE).
  */
 gret_status_t gret_paged_fork(
     const int32_t* src, const int32_t* dst, int n, int32_t* seq_lens, int S, int32_t* page_table,

@@ -114,7 +114,7 @@ def test_infinite_value_of_a_light_key(d, H, G):
 def test_long_sums_are_not_cut_off(H, G, d):
     """300 rows read the same 65536 keys, some 16000 a warp, whose values are all positive.  Sums that
     are rounded to 32 bits are off to either side, ones that are cut off all to one: 2048 steps that
-    lose a third of 2^-23 of what is summed up by then, half of the whole on average, make 4e-5.
+    lose 2^-23 or so of what is summed up by then, half of the whole on average, make 1.1e-4.
 
     The outputs, 1 to 2, are rounded to multiples of 2^-7 and spread over several of them (scores
     that vary by 2.5 leave some hundred keys that count), so the mean of N errors has a deviation of
