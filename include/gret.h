@@ -389,7 +389,8 @@ gret_status_t gret_paged_attention_decode(
  * the row b with cu_seqlens[b] <= i < cu_seqlens[b + 1] (int32 [S + 1], device) and goes to
  * position pos[b] + i - cu_seqlens[b]; tokens before the first and behind the last sequence are
  * left alone.  cu_seqlens NULL: T = S, token i goes to position pos[i] of row i.  Rows with pos < 0
- * are skipped (pos as gret_paged_resize gives it).
+ * are skipped (pos as gret_paged_resize gives it), tokens past the table (BAD_LENGTH) or on a page
+ * that is none (BAD_PAGE) too.
  *   k, v   [T, Hkv, d], token i, head h at i * k_stride_tok + h * k_stride_head elements (v
  *          likewise); 16-byte aligned.
  */
@@ -407,8 +408,9 @@ gret_status_t gret_paged_append(
  * its old length, where gret_paged_append puts the new tokens.  If its last page is partly filled
  * and shared (ref > 1), the row first gets a page of its own in its place with a copy of the slots
  * in use (copy on write).  A row that shrinks drops the pages past its new length (ref - 1, entry
- * -1), and one shrunk to 0 has given everything back.  Pages dropped by a call can be taken from
- * the next call on.  Not grown, and left as they are with pos = -1: a row past max_pages
+ * -1; an entry that is no page is BAD_PAGE, a count that was 0 already BAD_COUNT), and one shrunk to
+ * 0 has given everything back.  Pages dropped by a call can be taken from the next call on.  Rows
+ * whose length the table cannot hold stay as they are (BAD_LENGTH).  Not grown, and left as they are with pos = -1: a row past max_pages
  * (TABLE_FULL), a row whose partly filled last page is no page or has ref 0 (BAD_PAGE, BAD_COUNT),
  * and a row that needs pages when those asked for by the rows up to it exceed the pages that are
  * free (NO_PAGES).  pos = -1 for every row that does not grow.  pos shares no memory with delta,
@@ -440,7 +442,8 @@ gret_status_t gret_paged_fork(
  * the k-th page in use past index L moves to the k-th free page below L; ref and the table's
  * entries follow.  Pages from L on are free afterwards, so that their memory can be given up.  An
  * entry that names a page with ref 0 stays as it is (BAD_COUNT): the page is free, and another may
- * have been moved onto it.
+ * have been moved onto it.  So do entries that are no page (BAD_PAGE) and rows whose length the table
+ * cannot hold (BAD_LENGTH).
  */
 size_t gret_paged_compact_workspace_size(int n_pages);
 gret_status_t gret_paged_compact(
