@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(NT, APPLY_SM) resize_apply_kernel(const PagedR
 }
 
 // ---------------------------------------------------------------------------------------------
-// fork.  Bound by latency: 64 rows of 50 entries take 2.6 us, 512 of 7000 11.5, of which the copy of
+// fork.  Bound by latency: 64 rows of 50 entries take 2.8 us, 512 of 7000 11.8, of which the copy of
 // the 14 MB of entries would take 2.2.  The rest is the chain of every block before its first entry
 // (the pairs, the rows that they name, their lengths; and once more over all pairs for those that
 // share a source), then that of the second kernel.  Counts of pages that many rows share would be

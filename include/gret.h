@@ -408,13 +408,13 @@ gret_status_t gret_paged_append(
  * its old length, where gret_paged_append puts the new tokens.  If its last page is partly filled
  * and shared (ref > 1), the row first gets a page of its own in its place with a copy of the slots
  * in use (copy on write).  A row that shrinks drops the pages past its new length (ref - 1, entry
- * -1; an entry that is no page is BAD_PAGE, a count that was 0 already BAD_COUNT), and one shrunk to
- * 0 has given everything back.  Pages dropped by a call can be taken from the next call on.  Rows
- * whose length the table cannot hold stay as they are (BAD_LENGTH).  Not grown, and left as they are with pos = -1: a row past max_pages
- * (TABLE_FULL), a row whose partly filled last page is no page or has ref 0 (BAD_PAGE, BAD_COUNT),
- * and a row that needs pages when those asked for by the rows up to it exceed the pages that are
- * free (NO_PAGES).  pos = -1 for every row that does not grow.  pos shares no memory with delta,
- * seq_lens or ref (GRET_ERR_INVALID_ARG).
+ * -1; an entry that is no page is BAD_PAGE, a count that was 0 already BAD_COUNT), and one shrunk
+ * to 0 has given everything back.  Pages dropped by a call can be taken from the next call on.
+ * Rows whose length the table cannot hold stay as they are (BAD_LENGTH).  Not grown, and left as
+ * they are with pos = -1: a row past max_pages (TABLE_FULL), a row whose partly filled last page is
+ * no page or has ref 0 (BAD_PAGE, BAD_COUNT), and a row that needs pages when those asked for by
+ * the rows up to it exceed the pages that are free (NO_PAGES).  pos = -1 for every row that does
+ * not grow.  pos shares no memory with delta, seq_lens or ref (GRET_ERR_INVALID_ARG).
  */
 size_t gret_paged_resize_workspace_size(int S);
 gret_status_t gret_paged_resize(
